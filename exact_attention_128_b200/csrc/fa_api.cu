@@ -15,6 +15,9 @@
 #include "bwd_bf16.cuh"
 #include "bwd_d256.cuh"
 #include "bwd_f32.cuh"
+#include "qk_norm_rope.cuh"
+#include "decode_part.cuh"
+#include "evict.cuh"
 
 #ifndef FA_FWD_D64_BN
 #define FA_FWD_D64_BN 64
@@ -644,3 +647,5 @@ extern "C" fa_status fa_paged_decode_noalloc(const void* q, const void* k_cache,
   return fa_paged_decode(q, k_cache, v_cache, block_table, ctx_lens, o, lse, R, Hq, Hkv, d, block_size,
                          max_blocks_per_seq, num_blocks, scale, dtype, scratch, need, stream);
 }
+
+#include "ops_api.cuh"

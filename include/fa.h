@@ -239,6 +239,169 @@ fa_status fa_paged_decode_noalloc(const void* q, const void* k_cache, const void
                                   int num_blocks, float scale, fa_dtype dtype, void* stream);
 
 /*
+ * Norm and rotation of q and k — the pass before attention (no counterpart on the pages).
+ * Per head row x [d] with weight w [d] and n_axes positions per token:
+ *   r = (mean_c x_c^2 + eps)^(-1/2),  y = x r w;  without weights y = x,
+ *   each pair (a, b) of y turns by its angle t = positions[axis] * inv_freq[i]:
+ *   a' = a cos t - b sin t,  b' = a sin t + b cos t.
+ * Pair i of the rotary_dim / 2 pairs is (i, i + rotary_dim / 2), or (2i, 2i + 1) where
+ * interleaved is 1; values at and past rotary_dim do not turn.  The first sections[0] pairs
+ * follow axis 0 (time), the next sections[1] axis 1 (height), the last sections[2] axis 2
+ * (width); the n_axes sections (1 to 3, host array) sum to rotary_dim / 2.  Any int32 position
+ * is exact: the angle is reduced in 64 bits.  Products, sums and the norm are fp32, rounded
+ * once at the end.
+ *
+ * Common arguments:
+ *   q_strides, k_strides (, v_strides): host arrays {batch, head, token} in elements, multiples
+ *     of 16 bytes, so that views of a fused projection [B, N, heads, d] are read in place; a
+ *     head's d values are contiguous.  0 repeats a row.
+ *   q_weight, k_weight [d] of dtype `dtype`, or both NULL: no norm, the rotation alone.
+ *   positions int32: axis a, batch b, token n at a * pos_axis_stride + b * pos_batch_stride + n
+ *     (elements; a batch stride of 0 shares the positions).  inv_freq [rotary_dim / 2] double:
+ *     radians per position.
+ *   d in {64, 96, 128, 256}; rotary_dim a multiple of 16, at most d; eps > 0.
+ *   Outputs may not overlap inputs.
+ */
+
+/*
+ * fa_qk_norm_rope — q_out [B,Hq,N,d], k_out [B,Hkv,N,d] contiguous, as fa_fwd reads them; all
+ * of dtype `dtype` (F32 or BF16).
+ * Errors: FA_ERR_INVALID_ARG (null or misaligned pointer, bad size, stride, section, flag or
+ * eps, one weight without the other); FA_ERR_UNSUPPORTED (other d, rotary_dim or dtype).
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, const int64_t* q_strides, const int64_t* k_strides,
+                          const void* q_weight, const void* k_weight, const int* positions, int64_t pos_axis_stride,
+                          int64_t pos_batch_stride, const double* inv_freq, void* q_out, void* k_out, int B, int Hq,
+                          int Hkv, int N, int d, int rotary_dim, const int* sections, int n_axes, int interleaved,
+                          float eps, fa_dtype dtype, void* stream);
+
+/*
+ * fa_qk_norm_rope_append — the serving form: the same on R requests, with k' and v written
+ * straight into the paged cache.  Lengths as in fa_paged_prefill: request r's tokens are the last
+ * q_lens[r] positions of its ctx_lens[r] cached ones (0 <= q_lens[r] <= min(Nq_max, ctx_lens[r])),
+ * so token i goes to cache position ctx_lens[r] - q_lens[r] + i; a decode step has Nq_max = 1 and
+ * q_lens 1 (0: nothing to do for that request).  `positions` are the rotary ones: they need not
+ * be cache positions (after an eviction they are not).
+ *   q [R,Hq,Nq_max,d], k, v [R,Hkv,Nq_max,d] by strides, bf16; q_out [R,Hq,Nq_max,d] contiguous
+ *   (the q of fa_paged_prefill, and for Nq_max = 1 that of the decode calls).  Rows i >=
+ *   q_lens[r] are neither read nor written.
+ *   k_cache, v_cache [num_blocks,Hkv,block_size,d], block_table [R,max_blocks_per_seq], ctx_lens,
+ *   q_lens [R] int32 (device).  d in {64, 96, 128}, block_size == 16, dtype BF16.
+ *   A length out of range skips the request, a block id out of range skips the token's cache
+ *   write; either sets the device status word (FA_ERR_INVALID_ARG).  No two tokens of a call may
+ *   share a cache slot.
+ */
+fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, const int64_t* q_strides,
+                                 const int64_t* k_strides, const int64_t* v_strides, const void* q_weight,
+                                 const void* k_weight, const int* positions, int64_t pos_axis_stride,
+                                 int64_t pos_batch_stride, const double* inv_freq, void* k_cache, void* v_cache,
+                                 const int* block_table, const int* ctx_lens, const int* q_lens, void* q_out, int R,
+                                 int Hq, int Hkv, int Nq_max, int d, int block_size, int max_blocks_per_seq,
+                                 int num_blocks, int rotary_dim, const int* sections, int n_axes, int interleaved,
+                                 float eps, fa_dtype dtype, void* stream);
+
+/* fa_qk_norm_rope_bwd_workspace_size — bytes of device workspace fa_qk_norm_rope_bwd needs for its
+ * partial weight gradients (none without weights).  Returns 0 for an invalid d. */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * fa_qk_norm_rope_bwd — gradients of fa_qk_norm_rope, recomputing the norm from q and k.
+ *   dq_out [B,Hq,N,d], dk_out [B,Hkv,N,d] contiguous, of dtype dout_dtype (what fa_bwd writes).
+ *   q, k by strides, of dtype `dtype` (without weights only their type matters; they may be NULL).
+ *   dq, dk of dtype grad_dtype by dq_strides, dk_strides (the projection's layout, for example);
+ *   strides of dimensions larger than 1 must be at least d, and no two rows may share memory.
+ *   dq_weight, dk_weight [d] fp32: the sums over every row of q, of k (with weights only).  The
+ *   order of each sum is fixed: the same call gives the same bits.
+ *   dtype BF16: dout_dtype and grad_dtype each F32 or BF16.  dtype F32: both F32.
+ *   workspace: at least fa_qk_norm_rope_bwd_workspace_size(d) bytes, 256-byte aligned.
+ * Errors: as fa_qk_norm_rope, plus FA_ERR_WORKSPACE.
+ */
+fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, fa_dtype dout_dtype, const void* q, const void* k,
+                              const int64_t* q_strides, const int64_t* k_strides, const void* q_weight,
+                              const void* k_weight, const int* positions, int64_t pos_axis_stride,
+                              int64_t pos_batch_stride, const double* inv_freq, void* dq, void* dk,
+                              const int64_t* dq_strides, const int64_t* dk_strides, fa_dtype grad_dtype, float* dq_weight,
+                              float* dk_weight, int B, int Hq, int Hkv, int N, int d, int rotary_dim,
+                              const int* sections, int n_axes, int interleaved, float eps, fa_dtype dtype,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* fa_paged_decode_shared_workspace_size — bytes of device workspace fa_paged_decode_shared needs
+ * for its partial results.  Returns 0 for invalid sizes. */
+size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int max_prefix_blocks,
+                                             int max_blocks_per_seq, int block_size);
+
+/*
+ * fa_paged_decode_shared — one decode step of R requests that share a prefix.  Request r attends
+ * to the prefix's prefix_len[0] tokens and then to its own ctx_lens[r] ones; the prefix is read
+ * and multiplied once for all requests, and the two partial results are merged by their mass.
+ *   q [R,Hq,d] bf16; caches as in fa_paged_decode; prefix_table [max_prefix_blocks] and
+ *   block_table [R,max_blocks_per_seq] int32; prefix_len [1], ctx_lens [R] int32 (device).
+ *   Either length may be 0, up to its table's capacity; a request with no token at all gets
+ *   o = 0 and lse = -inf.  Table entries past a length's last block are never read.
+ *   o [R,Hq,d] bf16, lse [R,Hq] fp32 or NULL (natural log).
+ *   d in {64, 128}, block_size == 16, Hq / Hkv <= 16, dtype BF16.
+ *   A length out of range or a bad block id is not dereferenced and sets the device status word
+ *   (FA_ERR_INVALID_ARG); the results it belongs to are undefined.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.
+ */
+fa_status fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int* prefix_table,
+                                 const int* prefix_len, const int* block_table, const int* ctx_lens, void* o, float* lse,
+                                 int R, int Hq, int Hkv, int d, int block_size, int max_prefix_blocks,
+                                 int max_blocks_per_seq, int num_blocks, float scale, fa_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* fa_paged_decode_scored_workspace_size — bytes of device workspace fa_paged_decode_scored needs
+ * for its partial results and scores.  Returns 0 for invalid sizes. */
+size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int max_blocks_per_seq, int block_size);
+
+/*
+ * fa_paged_decode_scored — a decode step (as fa_paged_decode; ctx_lens[r] may be 0: o = 0,
+ * lse = -inf) that also adds up how much attention each cached token gets:
+ *   weights[r, hkv, s] += sum over the query heads of hkv of e^{score_s - lse},  s < ctx_lens[r].
+ *   weights [R, Hkv, max_blocks_per_seq * 16] fp32 by logical position, read and written; slots
+ *   at and past ctx_lens[r] are left as they are.  Each slot is added to once, by one thread: the
+ *   same call gives the same bits.
+ *   d in {64, 128}, block_size == 16, Hq / Hkv <= 16, dtype BF16.
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.
+ */
+fa_status fa_paged_decode_scored(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                                 const int* ctx_lens, float* weights, void* o, float* lse, int R, int Hq, int Hkv,
+                                 int d, int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                 fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* fa_paged_evict_workspace_size — bytes of device workspace fa_paged_evict needs for its lists of
+ * moves.  Returns 0 for invalid sizes. */
+size_t fa_paged_evict_workspace_size(int R, int Hkv, int max_blocks_per_seq, int keep);
+
+/*
+ * fa_paged_evict — shrink each request's cache to `keep` tokens per kv head: the tokens among the
+ * `recent` newest positions of its sequence, then the heaviest of the others by `weights` (ties:
+ * the lower slot; -0 is 0, NaN lighter than anything).  0 <= recent <= keep, keep >= 1.  A request
+ * with ctx_lens[r] <= keep loses nothing.
+ *   Kept tokens in slots below `keep` stay; the i-th kept token at or past `keep` moves into the
+ *   i-th freed slot below it, key and value (attention does not depend on the order of its keys;
+ *   keys carry their rotation with them).  Each kv head keeps its own tokens.
+ *   seq_lens [R] int32: tokens of the sequence so far, those evicted earlier among them
+ *   (>= ctx_lens[r]).  slot_pos [R, Hkv, max_blocks_per_seq * 16] int32: the sequence position of
+ *   the token in each slot, or negative for a slot filled by appending since the last eviction
+ *   (its position is then seq_lens[r] - ctx_lens[r] + slot); start with -1 everywhere.
+ *   weights as fa_paged_decode_scored keeps them.
+ *   weights_out, slot_pos_out (same shapes, whole): each kept token's weight and position in its
+ *   slot; 0 and -1 in every other slot, ready for tokens appended later.  new_ctx [R] =
+ *   min(ctx_lens[r], keep).  They may not alias the inputs.
+ *   k_cache, v_cache [num_blocks, Hkv, block_size, d] bf16, changed in place; a request's blocks
+ *   must be its own (a shared prefix stays outside its block_table).
+ *   d in {64, 96, 128, 256}, block_size == 16, dtype BF16.
+ *   A length out of range leaves the request as it is, a block id out of range skips that move;
+ *   either sets the device status word (FA_ERR_INVALID_ARG).
+ * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.
+ */
+fa_status fa_paged_evict(void* k_cache, void* v_cache, const int* block_table, const int* ctx_lens, const int* seq_lens,
+                         const float* weights, const int* slot_pos, float* weights_out, int* slot_pos_out, int* new_ctx,
+                         int R, int Hkv, int d, int block_size, int max_blocks_per_seq, int num_blocks, int keep,
+                         int recent, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fa_device_status — synchronises the current device and returns the device status
  * word the kernels set when a bounded wait runs out (FA_ERR_DEVICE_TIMEOUT) or a
  * block-table entry is out of range (FA_ERR_INVALID_ARG); FA_OK if none.  With

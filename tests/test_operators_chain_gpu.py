@@ -1,0 +1,203 @@
+"""The passes around attention as they are used together: a training step's rotation, attention and gradients; a
+serving loop that appends, decodes with weights and evicts; the same step captured and replayed; a shared prefix."""
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_128_b200 as fa
+from exact_attention_128_b200.workloads import randn
+from oracle import attention_fp64 as ora
+from oracle import operators_fp64 as ops
+from parity import check_bf16_stored
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def weights(d, seed):
+    return [(1 + 0.2 * randn((d,), seed + i, torch.float32)).to(BF).cuda() for i in (0, 1)]
+
+
+def test_training_step():
+    B, Hq, Hkv, N, d = 2, 4, 2, 130, 64
+    proj = randn((B, N, Hq + 2 * Hkv, d), 1, BF).cuda()
+    q, k, v = (t.transpose(1, 2) for t in proj.split([Hq, Hkv, Hkv], 2))
+    wq, wk = weights(d, 2)
+    pos, freq = torch.arange(N, device="cuda", dtype=torch.int32), fa.rope_frequencies(d)
+    do = randn((B, Hq, N, d), 4, BF).cuda()
+    q2, k2 = fa.qk_norm_rope(q, k, wq, wk, pos, freq)
+    vc = v.contiguous()
+    o, lse = fa.fwd(q2, k2, vc, causal=True)
+    dq2, dk2, dv = fa.bwd(q2, k2, vc, o, lse, do, causal=True)
+    dq, dk, dwq, dwk = fa.qk_norm_rope_bwd(dq2, dk2, q, k, wq, wk, pos, freq)
+    torch.cuda.synchronize()
+    P = np.broadcast_to(pos.cpu().numpy(), (1, B, N))
+    O, _ = ora.attention_fwd(q2, k2, vc, d**-0.5, True)
+    check_bf16_stored(o, O, "o")
+    rq, rk, _ = ora.attention_bwd(q2, k2, vc, do, d**-0.5, True)
+    for got, ref, x, w, dw in ((dq, rq, q, wq, dwq), (dk, rk, k, wk, dwk)):
+        dx, rw = ops.norm_rope_bwd(ref, x, w, P, freq, (32,), False, 1e-6)
+        check_bf16_stored(got, dx, "gradient")
+        assert np.linalg.norm(dw.cpu().numpy() - rw) <= 5e-3 * np.linalg.norm(rw)
+
+
+class Server:
+    """One layer's state: caches, lengths, weights, positions."""
+
+    def __init__(self, R=3, Hq=6, Hkv=2, d=128, maxb=5):
+        self.R, self.Hq, self.Hkv, self.d, self.maxb = R, Hq, Hkv, d, maxb
+        dev = dict(device="cuda")
+        self.table = torch.randperm(R * maxb, generator=torch.Generator().manual_seed(3)).view(R, maxb).int().cuda()
+        self.kc, self.vc = (torch.full((R * maxb, Hkv, 16, d), float("nan"), dtype=BF, **dev) for _ in range(2))
+        self.w = torch.zeros(R, Hkv, maxb * 16, **dev)
+        self.sp = torch.full((R, Hkv, maxb * 16), -1, dtype=torch.int32, **dev)
+        self.ctx = torch.zeros(R, dtype=torch.int32, **dev)
+        self.seq = torch.zeros(R, dtype=torch.int32, **dev)
+        self.wq, self.wk = weights(d, 20)
+        self.freq = fa.rope_frequencies(d)
+
+    def token(self, proj, lens):
+        """proj [R,N,heads,d]; lens [R]: append, and rotate q."""
+        q, k, v = (t.transpose(1, 2) for t in proj.split([self.Hq, self.Hkv, self.Hkv], 2))
+        N = proj.shape[1]
+        pos = (self.seq[:, None] + torch.arange(N, device="cuda", dtype=torch.int32)).int()
+        self.ctx += lens
+        self.seq += lens
+        return fa.qk_norm_rope_append(q, k, v, self.wq, self.wk, pos, self.freq, self.kc, self.vc, self.table, self.ctx,
+                                      lens)
+
+    def step(self, proj, lens):
+        q = self.token(proj, lens)
+        return fa.paged_decode_scored(q[:, :, 0], self.kc, self.vc, self.table, self.ctx, self.w)
+
+    def evict(self, keep, recent):
+        self.ctx, self.w, self.sp = fa.paged_evict(self.kc, self.vc, self.table, self.ctx, self.seq, self.w, self.sp,
+                                                   keep, recent)
+
+
+def test_serving_loop_with_eviction():
+    """Prompts, then steps with an eviction every 8: each step's output is attention over exactly the tokens kept."""
+    s = Server()
+    R, Hkv, d, keep, recent = s.R, s.Hkv, s.d, 32, 12
+    lens = torch.tensor([40, 7, 25], device="cuda", dtype=torch.int32)
+    prompt = randn((R, 40, 10, d), 30, BF).cuda()
+    q = s.token(prompt, lens)
+    o, _ = fa.paged_prefill(q, s.kc, s.vc, s.table, s.ctx, lens, causal=True)
+    torch.cuda.synchronize()
+    # every token's key and value by its sequence position
+    keys = [[{} for _ in range(Hkv)] for _ in range(R)]
+
+    def note(r, h, p, slot):
+        b, i = int(s.table[r, slot // 16]), slot % 16
+        keys[r][h][p] = (s.kc[b, h, i].clone(), s.vc[b, h, i].clone())
+
+    for r in range(R):
+        for h in range(Hkv):
+            for p in range(int(lens[r])):
+                note(r, h, p, p)
+    one = torch.ones(R, device="cuda", dtype=torch.int32)
+    for t in range(20):
+        s.step(randn((R, 1, 10, d), 40 + t, BF).cuda(), one)
+        for r in range(R):
+            for h in range(Hkv):
+                note(r, h, int(s.seq[r]) - 1, int(s.ctx[r]) - 1)
+        if t % 8 == 7:
+            s.evict(keep, recent)
+            n = s.ctx.tolist()
+            assert n == [min(a, keep) for a in (s.seq - (s.seq - torch.tensor(n, device="cuda"))).tolist()]
+            for r in range(R):
+                for h in range(Hkv):
+                    kept = s.sp[r, h, : n[r]].tolist()
+                    if int(s.seq[r]) > n[r]:
+                        assert set(range(int(s.seq[r]) - recent, int(s.seq[r]))) <= set(kept)
+                    if min(kept) >= 0:
+                        for slot, p in enumerate(kept):
+                            b, i = int(s.table[r, slot // 16]), slot % 16
+                            assert torch.equal(s.kc[b, h, i], keys[r][h][p][0])
+                            assert torch.equal(s.vc[b, h, i], keys[r][h][p][1])
+                    assert (s.w[r, h, n[r] :] == 0).all()
+    # the heads' weights of one more step sum to the group size, over live slots only
+    w0 = s.w.clone()
+    o, lse = s.step(randn((R, 1, 10, d), 99, BF).cuda(), one)
+    got = (s.w - w0).sum(-1).cpu()
+    assert torch.allclose(got, torch.full_like(got, 3.0), atol=1e-3)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert fa.device_status() == 0
+
+
+def test_step_replays_in_graphs():
+    """Append + scored decode + eviction captured in two graphs that share a memory pool, replayed in turn."""
+    a, b = Server(), Server()
+    R, d = a.R, a.d
+    proj = torch.empty(R, 1, 10, d, device="cuda", dtype=BF)
+    one = torch.ones(R, device="cuda", dtype=torch.int32)
+
+    def fill(s):
+        s.token(randn((R, 30, 10, d), 60, BF).cuda(), torch.tensor([30, 18, 24], device="cuda", dtype=torch.int32))
+
+    fill(a)
+    fill(b)
+    dev = dict(device="cuda")
+    w2, sp2, n2 = torch.empty_like(a.w), torch.empty_like(a.sp), torch.empty_like(a.ctx)
+    out = [torch.empty(R, a.Hq, d, dtype=BF, **dev) for _ in range(2)]
+
+    def body(s, o):
+        q, k, v = (t.transpose(1, 2) for t in proj.split([s.Hq, s.Hkv, s.Hkv], 2))
+        s.ctx += one
+        s.seq += one
+        q2 = fa.qk_norm_rope_append(q, k, v, s.wq, s.wk, (s.seq - 1)[:, None], s.freq, s.kc, s.vc, s.table, s.ctx, one)
+        fa.paged_decode_scored(q2[:, :, 0], s.kc, s.vc, s.table, s.ctx, s.w, out=o)
+        fa.paged_evict(s.kc, s.vc, s.table, s.ctx, s.seq, s.w, s.sp, 22, 6, weights_out=w2, slot_pos_out=sp2, new_ctx=n2)
+        s.w.copy_(w2)
+        s.sp.copy_(sp2)
+        s.ctx.copy_(n2)
+
+    proj.copy_(randn((R, 1, 10, d), 70, BF))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # warm-up on another stream than the current one
+        scratch = Server()
+        fill(scratch)
+        body(scratch, out[0])
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    with torch.cuda.graph(graphs[0]):
+        body(a, out[0])
+    with torch.cuda.graph(graphs[1], pool=graphs[0].pool()):
+        body(a, out[1])
+    for t in range(6):
+        proj.copy_(randn((R, 1, 10, d), 71 + t, BF))
+        graphs[t % 2].replay()
+        got = out[t % 2].clone()
+        ref = torch.empty_like(got)
+        body(b, ref)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref), t
+        for x, y in ((a.kc, b.kc), (a.vc, b.vc)):
+            assert torch.equal(x.nan_to_num(), y.nan_to_num())
+        assert torch.equal(a.w, b.w) and torch.equal(a.sp, b.sp) and torch.equal(a.ctx, b.ctx)
+    assert fa.device_status() == 0
+
+
+def test_shared_prefix_step_equals_the_copied_prefix():
+    """Requests behind one prompt: the shared call equals a decode whose table repeats the prompt's blocks."""
+    R, Hq, Hkv, d, P = 9, 12, 2, 128, 208
+    g = torch.Generator().manual_seed(4)
+    ids = torch.randperm(200, generator=g).int()
+    pre, table = ids[: P // 16], ids[20 : 20 + R * 4].view(R, 4).contiguous()
+    kc, vc = (randn((200, Hkv, 16, d), 5 + i, BF).cuda() for i in (0, 1))
+    wq, wk = weights(d, 7)
+    ctx = torch.randint(0, 60, (R,), generator=g).int().cuda()
+    proj = randn((R, 1, Hq + 2 * Hkv, d), 8, BF).cuda()
+    q, k, v = (t.transpose(1, 2) for t in proj.split([Hq, Hkv, Hkv], 2))
+    ctx += 1
+    q = fa.qk_norm_rope_append(q, k, v, wq, wk, (P + ctx - 1)[:, None], fa.rope_frequencies(d), kc, vc, table.cuda(),
+                               ctx, torch.ones_like(ctx))[:, :, 0]
+    o, lse = fa.paged_decode_shared(q, kc, vc, pre.cuda(), torch.tensor([P], device="cuda", dtype=torch.int32),
+                                    table.cuda(), ctx)
+    joined = torch.cat([pre[None].expand(R, -1), table], 1).contiguous().cuda()
+    o2, lse2 = fa.paged_decode(q, kc, vc, joined, ctx + P)
+    torch.cuda.synchronize()
+    assert (o.float() - o2.float()).abs().max() <= 2e-2 and (lse - lse2).abs().max() <= 1e-4
+    assert fa.device_status() == 0
