@@ -2,6 +2,15 @@
 // position rotation, the decode steps over pieces of the cache, and the eviction.  Included by
 // fa_api.cu, whose helpers (alignment, TMA descriptors, launches) it uses.
 #pragma once
+#ifndef FA_ROPE_PERSM
+#define FA_ROPE_PERSM 32
+#endif
+#ifndef FA_ROPE_BWD_PERSM
+#define FA_ROPE_BWD_PERSM 32
+#endif
+#ifndef FA_ROPE_BWD_C
+#define FA_ROPE_BWD_C 2
+#endif
 
 namespace {
 
@@ -35,11 +44,13 @@ bool rope_rows(const void* p, const int64_t* strides, fa_dtype dtype) {
   return true;
 }
 
-// Tokens per CTA: as many as keep every SM's share of CTAs, so that one new token per request
-// spreads over the SMs and long inputs amortise the CTA's set-up.
-int rope_tok(int64_t tokens, int sms) {
-  const int64_t t = tokens / (int64_t(sms) * 8);
-  return int(std::max<int64_t>(1, std::min<int64_t>(rope::MAX_TOK, t)));
+// Heads per unit of work: 16, halved until every SM has `per_sm` units (or a head is a unit),
+// and spread evenly over the heads.
+int rope_chunk(int64_t rows, int tokens_per_warp, int H, int per_sm, int sms) {
+  int c = rope::MAX_CHUNK;
+  while (c > 1 && rows / (int64_t(tokens_per_warp) * c) < int64_t(per_sm) * sms) c /= 2;
+  const int chunks = (H + c - 1) / c;
+  return (H + chunks - 1) / chunks;
 }
 
 template <typename T, int D, bool PAGED>
@@ -47,32 +58,47 @@ fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return FA_ERR_CUDA;
   const int64_t tokens = int64_t(prm.B) * prm.N;
-  prm.tok = rope_tok(tokens, sms);
-  const int64_t grid = (tokens + prm.tok - 1) / prm.tok;
-  if (grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  constexpr int TOKENS = rope::Cfg<D>::TOKENS;
+  const int heads = prm.Hq + (PAGED ? 2 : 1) * prm.Hkv;
+  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.Hq, FA_ROPE_PERSM, sms);
+  prm.chunks_q = (prm.Hq + prm.chunk - 1) / prm.chunk;
+  prm.chunks_k = (prm.Hkv + prm.chunk - 1) / prm.chunk;
+  const int64_t units = (tokens + TOKENS - 1) / TOKENS * (prm.chunks_q + (PAGED ? 2 : 1) * prm.chunks_k);
+  const int64_t grid = (units + rope::THREADS / 32 - 1) / (rope::THREADS / 32);
+  if (tokens > 0x7fffff00 || grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
   auto kern = inter ? fa_qk_norm_rope_kernel<T, D, true, PAGED> : fa_qk_norm_rope_kernel<T, D, false, PAGED>;
-  if (launch_pdl(kern, dim3(unsigned(grid)), dim3(rope::THREADS), 0, st, prm) != cudaSuccess) return FA_ERR_CUDA;
+  constexpr int SMEM = rope::STAGES * rope::Slot<T, sizeof(T) == 4>::BYTES;
+  if (set_smem(kern, SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(unsigned(grid)), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess) return FA_ERR_CUDA;
   return launched();
 }
 
-constexpr int kRopeBwdCtas = 148 * 4;  // CTAs of the backward kernel, at most
+constexpr int kRopeBwdCtas = 148 * FA_ROPE_BWD_C;  // CTAs of the backward kernel, at most
 
 template <typename T, typename TG, typename TO, int D>
 fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk, cudaStream_t st) {
   const int64_t tokens = int64_t(prm.B) * prm.N;
-  prm.tok = rope_tok(tokens, kRopeBwdCtas / 4);
-  const int64_t tiles = (tokens + prm.tok - 1) / prm.tok;
-  // CTAs in proportion to the rows of q and of k, no more than there are tiles
-  const int total = kRopeBwdCtas;
-  int nq = int(int64_t(total) * prm.H[0] / (prm.H[0] + prm.H[1]));
-  nq = std::max(1, std::min(total - 1, nq));
-  int nk = int(std::min<int64_t>(tiles, total - nq));
-  nq = int(std::min<int64_t>(tiles, nq));
-  prm.ctas_q = nq;
+  if (tokens > 0x7fffff00) return FA_ERR_UNSUPPORTED;
+  constexpr int TOKENS = rope::Cfg<D>::TOKENS, WARPS = rope::THREADS / 32;
+  const int heads = prm.H[0] + prm.H[1];
+  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.H[0], FA_ROPE_BWD_PERSM, kRopeBwdCtas / FA_ROPE_BWD_C);
+  int ctas[2];
+  for (int k = 0; k < 2; ++k) {
+    prm.chunks[k] = (prm.H[k] + prm.chunk - 1) / prm.chunk;
+    // CTAs in proportion to the rows, no more than there are units
+    const int64_t units = (tokens + TOKENS - 1) / TOKENS * prm.chunks[k];
+    const int64_t share = std::max<int64_t>(1, int64_t(kRopeBwdCtas) * prm.H[k] / heads);
+    ctas[k] = int(std::min<int64_t>(std::min<int64_t>(share, kRopeBwdCtas - 1), (units + WARPS - 1) / WARPS));
+  }
+  prm.ctas_q = ctas[0];
   auto kern = inter ? fa_qk_norm_rope_bwd_kernel<T, TG, TO, D, true> : fa_qk_norm_rope_bwd_kernel<T, TG, TO, D, false>;
-  if (launch_pdl(kern, dim3(unsigned(nq + nk)), dim3(rope::THREADS), 0, st, prm) != cudaSuccess) return FA_ERR_CUDA;
-  if (prm.w[0] && launch_pdl(fa_qk_norm_rope_dw_kernel, dim3(2), dim3(256), 0, st, static_cast<const float*>(prm.part),
-                             dwq, dwk, D, nq, nq + nk) != cudaSuccess)
+  constexpr int SMEM = rope::BWD_STAGES * rope::THREADS * 16 * int(sizeof(T) + sizeof(TG));
+  static_assert(SMEM >= WARPS * D * 4, "the weight-gradient sums reuse the slots");
+  if (set_smem(kern, SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_pdl(kern, dim3(unsigned(ctas[0] + ctas[1])), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
+    return FA_ERR_CUDA;
+  if (prm.w[0] && launch_pdl(fa_qk_norm_rope_dw_kernel, dim3(D / 8, 2), dim3(512), 0, st,
+                             static_cast<const float*>(prm.part), dwq, dwk, D, ctas[0], ctas[0] + ctas[1]) != cudaSuccess)
     return FA_ERR_CUDA;
   return launched();
 }
@@ -225,7 +251,7 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, const int64_t* q_strides
                  positions, inv_freq,
                  {q_out, k_out},
                  pos_axis_stride, pos_batch_stride, B, Hq, Hkv, N, rotary_dim, sections[0],
-                 n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1,
+                 n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, 1, 1,
                  nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == FA_DTYPE_BF16 ? rope_by_d<__nv_bfloat16>(prm, d, interleaved, st)
@@ -261,7 +287,7 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, co
                  positions, inv_freq,
                  {q_out, nullptr},
                  pos_axis_stride, pos_batch_stride, R, Hq, Hkv, Nq_max, rotary_dim, sections[0],
-                 n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1,
+                 n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, 1, 1,
                  block_table, ctx_lens, q_lens, k_cache, v_cache, max_blocks_per_seq, num_blocks};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (d) {
@@ -317,7 +343,7 @@ fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, fa_dtype d
                     {dq_strides[2], dk_strides[2]},
                     static_cast<float*>(workspace),
                     pos_axis_stride, pos_batch_stride, B, {Hq, Hkv}, N, rotary_dim, sections[0],
-                    n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, 0};
+                    n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, {1, 1}, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == FA_DTYPE_F32) return rope_bwd_by_d<float, float, float>(prm, d, interleaved, dq_weight, dk_weight, st);
   using bf = __nv_bfloat16;

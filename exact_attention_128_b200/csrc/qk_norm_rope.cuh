@@ -8,10 +8,13 @@
 // h = g w,  dx = r (h - n mean_c(h n)).
 //
 // What bounds it: device memory.  Each value is read once and written once (backward: dy and x
-// read, dx written) for about 10 operations.  A row of d values is held by d/16 lanes, two
-// 16-byte pieces each, chosen so that both members of every pair sit in one lane: no value moves
-// between lanes but the row's sum of squares.  A CTA works on `tok` tokens and computes their
-// cosines and sines once, for all heads, into shared memory.
+// read, dx written) for about 10 operations.  A row of d values is held by d/16 lanes, four runs
+// of 4 values each, chosen so that both members of every pair sit in one lane: no value moves
+// between lanes but the row's sum of squares.  A group of lanes stays with one token and walks
+// heads: the token's cosines and sines and the head weights are computed and read once and stay
+// in registers, there is no shared memory and no barrier, and a warp writes 1 KB of consecutive
+// tokens of one head.  `chunk` heads make a unit of work, few when there are few tokens (a
+// decode step then has a row per group) and up to MAX_CHUNK, which amortises the cosines.
 //
 // Angles: the position (up to 2^31) times the frequency is taken in turns in 64 bits and reduced
 // to [-1/2, 1/2] before it is rounded to 32 bits, so far positions lose nothing; no table of
@@ -20,16 +23,30 @@
 #include "common.cuh"
 
 namespace fa {
+#ifndef FA_ROPE_STAGES
+#define FA_ROPE_STAGES 5
+#endif
+#ifndef FA_ROPE_MINB
+#define FA_ROPE_MINB 2
+#endif
+#ifndef FA_ROPE_BWD_STAGES
+#define FA_ROPE_BWD_STAGES 4
+#endif
+#ifndef FA_ROPE_BWD_MINB
+#define FA_ROPE_BWD_MINB 2
+#endif
 namespace rope {
 constexpr int THREADS = 256;
-constexpr int MAX_TOK = 8;
+constexpr int MAX_CHUNK = 16;  // heads of a unit, at most
+constexpr int STAGES = FA_ROPE_STAGES;          // forward: rows a thread has in flight, + 1
+constexpr int BWD_STAGES = FA_ROPE_BWD_STAGES;  // backward
 
 // Lanes of one row: d / 16 rounded up to a power of two (d = 96: 6 of 8 lanes work).
 template <int D>
 struct Cfg {
   static constexpr int PAIRS = D / 16;  // lanes that hold values
   static constexpr int L = D == 96 ? 8 : D / 16;
-  static constexpr int GROUPS = THREADS / L;  // rows a CTA holds at a time
+  static constexpr int TOKENS = 32 / L;  // tokens of a warp
 };
 }  // namespace rope
 
@@ -44,7 +61,8 @@ struct RopeParams {
   int B, Hq, Hkv, N;
   int rd, sec0, sec1;     // rotary dims; frequencies below sec0 follow axis 0, below sec1 axis 1, then axis 2
   float eps;
-  int tok;                // tokens per CTA
+  int chunk;              // heads per unit
+  int chunks_q, chunks_k; // units of a token group: of q, of k (and as many of v)
   // paged: cache rows of the tokens
   const int *bt, *ctx, *qlen;
   void *kc, *vc;
@@ -65,108 +83,162 @@ struct RopeBwdParams {
   int B, H[2], N;
   int rd, sec0, sec1;
   float eps;
-  int tok;
+  int chunk, chunks[2];
   int ctas_q;  // CTAs [0, ctas_q) take the rows of q, the others those of k
 };
 
 namespace rope {
 
-// Eight values as they are stored, and as fp32.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+// Packed fp32 pairs: one instruction for two values.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+__device__ __forceinline__ float2 unpack(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Where a lane's four runs of 4 values lie in a row (in runs): two in the first half of the
+// rotary width and their partners in the second; the runs behind the rotary width are dealt out
+// to the lanes behind it in the same way.  SPREAD: neighbouring lanes hold neighbouring runs, so
+// that an fp32 access of 16 bytes a lane fills its 32-byte sectors (with the bf16 layout, which
+// keeps two runs side by side for 16-byte accesses, fp32 asked L2 for each sector twice).
+template <int D, bool SPREAD>
+struct Runs {
+  int q[4];
+  __device__ __forceinline__ Runs(int c, int rd) {
+    const int p2 = rd / 16, m = D / 16 - p2;
+    const int base = c < p2 ? 0 : 4 * p2, w = c < p2 ? p2 : m, j = c < p2 ? c : c - p2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(a[i] << 16);
-      f[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) q[i] = base + (SPREAD ? i * w + j : (i >> 1) * 2 * w + 2 * j + (i & 1));
+  }
+};
+// A thread's 16 values of a row on their way from device memory: pieces in shared memory that
+// only this thread writes (cp.async) and reads, [piece][thread], so that rows in flight cost no
+// registers and no barrier.  Values are kept as 8 pairs, pairs 2i and 2i + 1 of run i.
+template <typename T, bool SPREAD>
+struct Slot {
+  static constexpr int N = SPREAD ? 4 : 2;                 // pieces
+  static constexpr int PIECE = 16 * int(sizeof(T)) / N;    // their bytes: 8 or 16
+  static constexpr int BYTES = N * PIECE * THREADS;        // of one row of every thread
+  static_assert(SPREAD || sizeof(T) == 2, "fp32 rows are spread");
+  // a row's values, or zeros
+  template <int D>
+  static __device__ __forceinline__ void fetch(uint32_t at, const T* row, const Runs<D, SPREAD>& r, bool on) {
+    const int bytes = on ? PIECE : 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const T* src = row + r.q[SPREAD ? i : 2 * i] * 4;
+      if constexpr (PIECE == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * THREADS * PIECE), "l"(src),
+                     "r"(bytes)
+                     : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(at + i * THREADS * PIECE), "l"(src),
+                     "r"(bytes)
+                     : "memory");
+    }
+  }
+  static __device__ __forceinline__ void read(uint32_t at, float2 (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint4 v;
+      if constexpr (PIECE == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(at + i * THREADS * PIECE));
+      else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at + i * THREADS * PIECE));
+      if constexpr (sizeof(T) == 4) {
+        f[2 * i] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[2 * i + 1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+      } else if constexpr (SPREAD) {
+        f[2 * i] = unpack(v.x);
+        f[2 * i + 1] = unpack(v.y);
+      } else {
+        f[4 * i] = unpack(v.x);
+        f[4 * i + 1] = unpack(v.y);
+        f[4 * i + 2] = unpack(v.z);
+        f[4 * i + 3] = unpack(v.w);
+      }
     }
   }
 };
-template <>
-struct Raw<float> {
-  float4 u, v;
-  __device__ __forceinline__ void load(const float* p) {
-    u = __ldg(reinterpret_cast<const float4*>(p));
-    v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+template <int D, bool SPREAD>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, const Runs<D, SPREAD>& r, const float2 (&f)[8]) {
+  if constexpr (SPREAD) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint2*>(row + r.q[i] * 4) =
+          make_uint2(pack_bf16x2(f[2 * i].x, f[2 * i].y), pack_bf16x2(f[2 * i + 1].x, f[2 * i + 1].y));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(row + r.q[2 * i] * 4) =
+          make_uint4(pack_bf16x2(f[4 * i].x, f[4 * i].y), pack_bf16x2(f[4 * i + 1].x, f[4 * i + 1].y),
+                     pack_bf16x2(f[4 * i + 2].x, f[4 * i + 2].y), pack_bf16x2(f[4 * i + 3].x, f[4 * i + 3].y));
   }
-  __device__ __forceinline__ void clear() { u = v = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-    f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+}
+template <int D>
+__device__ __forceinline__ void store_row(float* row, const Runs<D, true>& r, const float2 (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(row + r.q[i] * 4) = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+}
+// A lane's 16 weights.
+template <typename T, int D, bool SPREAD>
+__device__ __forceinline__ void load_weights(const void* w, const Runs<D, SPREAD>& r, float2 (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const T* at = static_cast<const T*>(w) + r.q[i >> 1] * 4 + 2 * (i & 1);
+    f[i] = make_float2(float(at[0]), float(at[1]));
   }
-};
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *(reinterpret_cast<float4*>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-
-// The two 8-value pieces of lane c: piece c and its partner a half rotary width behind it; the
-// pieces behind the rotary width are dealt out in the same way, to the lanes behind it.
-template <int D>
-__device__ __forceinline__ void pieces(int c, int rd, int& lo, int& hi) {
-  const int p2 = rd / 16;
-  lo = c < p2 ? c : p2 + c;
-  hi = c < p2 ? c + p2 : D / 16 + c;
+__device__ __forceinline__ void rows_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void rows_wait() {  // all but this thread's newest N rows are here
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A per-lane table of 8 values per lane is kept as two planes of [lane][4], so that a 16-byte
-// read of neighbouring lanes touches neighbouring banks.
-template <int D>
-__device__ __forceinline__ int slot(int c, int e) {
-  return ((e >> 2) * Cfg<D>::PAIRS + c) * 4 + (e & 3);
-}
-template <int D>
-__device__ __forceinline__ void read8(const float* t, int c, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(t + c * 4);
-  const float4 b = *reinterpret_cast<const float4*>(t + (Cfg<D>::PAIRS + c) * 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-
-// Cosine and sine of table entry i (lane i / 8, pair i % 8) of one token.  `pos` points at the
-// token's position on axis 0.  Lanes behind the rotary width get (1, 0).
-template <int D, bool INTER>
-__device__ __forceinline__ void angle(int i, const int* pos, int64_t pos_sa, const double* freq, int rd, int sec0,
-                                      int sec1, float& c, float& s) {
-  const int lane = i >> 3, e = i & 7, p2 = rd / 16;
-  c = 1.f;
-  s = 0.f;
-  if (lane >= p2) return;
-  const int f = INTER ? (e < 4 ? 4 * lane + e : 4 * (lane + p2) + e - 4) : i;
-  const int axis = f < sec0 ? 0 : f < sec1 ? 1 : 2;
-  const double turns = double(__ldg(pos + axis * pos_sa)) * (__ldg(freq + f) * 0.15915494309189533577);
-  sincospif(2.f * float(turns - rint(turns)), &s, &c);
+// Cosines and sines of a lane's 8 pairs for one token (lanes behind the rotary width: 1 and 0).
+// `pos` points at the token's position on axis 0.
+template <bool INTER, int D, bool SPREAD>
+__device__ __forceinline__ void angles(const Runs<D, SPREAD>& r, const int* pos, int64_t pos_sa, const double* freq,
+                                       int rd, int sec0, int sec1, float2 (&cs)[4], float2 (&sn)[4]) {
+  const bool turns_at_all = r.q[0] * 4 < rd;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float s = 0.f, c = 1.f;
+    if (turns_at_all) {
+      // pair e: adjacent values of run e / 2, or value e % 4 of run e / 4 with its partner
+      const int f = INTER ? r.q[e >> 1] * 2 + (e & 1) : r.q[e >> 2] * 4 + (e & 3);
+      const int axis = f < sec0 ? 0 : f < sec1 ? 1 : 2;
+      const double turns = double(__ldg(pos + axis * pos_sa)) * (__ldg(freq + f) * 0.15915494309189533577);
+      sincospif(2.f * float(turns - rint(turns)), &s, &c);
+    }
+    (e & 1 ? sn[e >> 1].y : sn[e >> 1].x) = s;
+    (e & 1 ? cs[e >> 1].y : cs[e >> 1].x) = c;
+  }
 }
 
+// Turn a lane's pairs: half-width pairs (runs 0, 1 with runs 2, 3) in packed form, adjacent ones
+// one by one.
 template <bool INTER>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void turn(float2 (&f)[8], const float2 (&c)[4], const float2 (&s)[4]) {
   if constexpr (INTER) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x0 = a[2 * e], x1 = a[2 * e + 1], y0 = b[2 * e], y1 = b[2 * e + 1];
-      a[2 * e] = x0 * c[e] - x1 * s[e];
-      a[2 * e + 1] = x0 * s[e] + x1 * c[e];
-      b[2 * e] = y0 * c[4 + e] - y1 * s[4 + e];
-      b[2 * e + 1] = y0 * s[4 + e] + y1 * c[4 + e];
+    for (int e = 0; e < 8; ++e) {
+      const float cc = e & 1 ? c[e >> 1].y : c[e >> 1].x, ss = e & 1 ? s[e >> 1].y : s[e >> 1].x;
+      // (x, y) -> x (c, s) + y (-s, c)
+      f[e] = fma2(both(f[e].x), make_float2(cc, ss), mul2(both(f[e].y), make_float2(-ss, cc)));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = a[e], y = b[e];
-      a[e] = x * c[e] - y * s[e];
-      b[e] = x * s[e] + y * c[e];
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = f[i], y = f[4 + i];
+      f[i] = fma2(x, c[i], neg2(mul2(y, s[i])));
+      f[4 + i] = fma2(x, s[i], mul2(y, c[i]));
     }
   }
 }
@@ -178,299 +250,232 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Weight tables of lane order: piece lo at [0], piece hi at [1].
-template <typename T, int D>
-__device__ __forceinline__ void fill_weights(float (*t)[D / 2], const void* w, int rd) {
-  for (int i = threadIdx.x; i < D; i += THREADS) {
-    const int half = i / (D / 2), j = i % (D / 2), c = j >> 3, e = j & 7;
-    int lo, hi;
-    pieces<D>(c, rd, lo, hi);
-    t[half][slot<D>(c, e)] = to_f32(static_cast<const T*>(w)[(half ? hi : lo) * 8 + e]);
-  }
-}
-
 }  // namespace rope
 
-// One CTA: `tok` consecutive tokens (of the B x N), all their heads.  Rows run head-fastest, so
-// the rows of a warp share a token's cosines and the reads of a fused projection are contiguous.
+// One warp per unit: 32 / L consecutive tokens (of the B x N) x `chunk` heads of q, k or v.
 // PAGED (bf16): token (r, i) of request r is one of its last q_lens[r] positions; q' goes to
 // [R, Hq, N, d], k' and v to cache position ctx_lens[r] - q_lens[r] + i; padding rows are left.
 template <typename T, int D, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(rope::THREADS) fa_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB) fa_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   using namespace rope;
   using C = Cfg<D>;
-  __shared__ float s_cos[MAX_TOK][D / 2], s_sin[MAX_TOK][D / 2];
-  __shared__ float s_w[2][2][D / 2];
-  __shared__ int64_t s_row[MAX_TOK];  // paged: cache row (block * Hkv * 16 + slot) of the token, -1: not cached
-  __shared__ int s_live[MAX_TOK];
-  const int64_t tokens = int64_t(p.B) * p.N;
-  const int64_t t0 = int64_t(blockIdx.x) * p.tok;
-  const int nt = int(min(int64_t(p.tok), tokens - t0));
-  const bool norm = p.w[0] != nullptr;
-  const int heads = p.Hq + p.Hkv + (PAGED ? p.Hkv : 0);
+  const int tokens = p.B * p.N;
+  const int per_group = p.chunks_q + (PAGED ? 2 : 1) * p.chunks_k;
+  const int64_t unit = int64_t(blockIdx.x) * (THREADS / 32) + warp_id();
+  const int tg = int(unit / per_group);
+  int chunk = int(unit - int64_t(tg) * per_group);
+  const int lane = lane_id(), c = lane % C::L;
+  const int t = tg * C::TOKENS + lane / C::L;
+  if (tg * C::TOKENS >= tokens) return;  // (the whole warp)
+  const int kind = chunk < p.chunks_q ? 0 : chunk < p.chunks_q + p.chunks_k ? 1 : 2;
+  if (kind > 0) chunk -= p.chunks_q + (kind - 1) * p.chunks_k;
+  const int H = kind == 0 ? p.Hq : p.Hkv;
+  const int h0 = chunk * p.chunk, h1 = min(H, h0 + p.chunk);
+  bool on = c < C::PAIRS && t < tokens;
+  const int b = on ? t / p.N : 0, n = on ? t - b * p.N : 0;
+  constexpr bool SPREAD = sizeof(T) == 4;
+  const Runs<D, SPREAD> runs(c < C::PAIRS ? c : 0, p.rd);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  int64_t row = 0;  // paged: cache row (block * Hkv * 16 + slot) of the token
   if constexpr (PAGED) {
-    int live = 0;
-    if (threadIdx.x < nt) {
-      const int64_t t = t0 + threadIdx.x;
-      const int r = int(t / p.N), i = int(t % p.N);
-      const int L = p.ctx[r], ql = p.qlen[r];
-      int64_t row = -1;
-      if (ql < 0 || ql > p.N || L < ql || L > p.max_blocks * 16) {
-        if (i == 0) set_status(FA_ERR_INVALID_ARG, 200);
-      } else if (i < ql) {
-        live = 1;
-        const int at = L - ql + i;
-        const int phys = p.bt[int64_t(r) * p.max_blocks + at / 16];
-        if (phys < 0 || phys >= p.num_blocks)
-          set_status(FA_ERR_INVALID_ARG, 201);
-        else
-          row = int64_t(phys) * p.Hkv * 16 + at % 16;
-      }
-      s_row[threadIdx.x] = row;
-      s_live[threadIdx.x] = live;
-    }
-    if (!__syncthreads_or(live)) return;
-  }
-  for (int i = threadIdx.x; i < nt * (D / 2); i += THREADS) {
-    const int tt = i / (D / 2), j = i % (D / 2);
-    const int64_t t = t0 + tt;
-    float c, s;
-    angle<D, INTER>(j, p.pos + (t / p.N) * p.pos_sb + t % p.N, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, c, s);
-    s_cos[tt][slot<D>(j >> 3, j & 7)] = c;
-    s_sin[tt][slot<D>(j >> 3, j & 7)] = s;
-  }
-  if (norm) {
-    fill_weights<T, D>(s_w[0], p.w[0], p.rd);
-    fill_weights<T, D>(s_w[1], p.w[1], p.rd);
-  }
-  __syncthreads();
-
-  const int c = threadIdx.x % C::L;
-  const bool lane_on = c < C::PAIRS;
-  int lo, hi;
-  pieces<D>(c, p.rd, lo, hi);
-  const int rows = nt * heads;
-  const int first = threadIdx.x / C::L;
-  const int warp_first = (threadIdx.x & ~31) / C::L;
-  for (int base = 0; base + warp_first < rows; base += C::GROUPS) {
-    const int row = base + first;
-    const int tt = row / heads, h = row - tt * heads;
-    bool on = lane_on && row < rows;
-    if constexpr (PAGED) on = on && s_live[tt];
-    const int64_t t = t0 + tt, b = t / p.N, n = t % p.N;
-    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
-    const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
-    Raw<T> ra, rb;
-    ra.clear();
-    rb.clear();
     if (on) {
-      const T* src = static_cast<const T*>(p.x[kind]) + b * p.sb[kind] + hh * p.sh[kind] + n * p.sn[kind];
-      ra.load(src + lo * 8);
-      rb.load(src + hi * 8);
-    }
-    float a[8], bb[8];
-    ra.get(a);
-    rb.get(bb);
-    if (norm) {
-      float sq = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sq += a[e] * a[e] + bb[e] * bb[e];
-      sq = row_sum<C::L>(sq);
-      if (on && kind < 2) {
-        const float r = rsqrtf(sq * (1.f / D) + p.eps);
-        float wa[8], wb[8];
-        read8<D>(s_w[kind][0], c, wa);
-        read8<D>(s_w[kind][1], c, wb);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e] *= r * wa[e];
-          bb[e] *= r * wb[e];
+      const int L = p.ctx[b], ql = p.qlen[b];
+      if (ql < 0 || ql > p.N || L < ql || L > p.max_blocks * 16) {
+        if (n == 0) set_status(FA_ERR_INVALID_ARG, 200);
+        on = false;
+      } else if (n >= ql) {
+        on = false;
+      } else if (kind > 0) {
+        const int at = L - ql + n;
+        const int phys = p.bt[int64_t(b) * p.max_blocks + at / 16];
+        if (phys < 0 || phys >= p.num_blocks) {
+          set_status(FA_ERR_INVALID_ARG, 201);
+          on = false;
+        } else {
+          row = int64_t(phys) * p.Hkv * 16 + at % 16;
         }
       }
     }
-    if (!on) continue;
-    if (kind < 2) {
-      float cs[8], sn[8];
-      read8<D>(s_cos[tt], c, cs);
-      read8<D>(s_sin[tt], c, sn);
-      turn<INTER>(a, bb, cs, sn);
+    if (!__any_sync(0xffffffffu, on)) return;
+  }
+  const T* src = static_cast<const T*>(p.x[kind]) + b * p.sb[kind] + n * p.sn[kind];
+  const int64_t sh = p.sh[kind];
+  T* dst;
+  int64_t dh;  // distance of two heads' rows
+  if (PAGED && kind > 0) {
+    dst = static_cast<T*>(kind == 1 ? p.kc : p.vc) + row * D;
+    dh = 16 * D;
+  } else {
+    dst = static_cast<T*>(p.out[kind == 0 ? 0 : 1]) + (int64_t(b) * H * p.N + n) * D;
+    dh = int64_t(p.N) * D;
+  }
+  // rows in flight: prologue, then one more for each row that is worked on
+  using R = Slot<T, SPREAD>;
+  extern __shared__ uint8_t rope_smem[];
+  const uint32_t slot = smem_u32(rope_smem) + threadIdx.x * R::PIECE;
+  auto fetch = [&](int i) {
+    if (h0 + i < h1) R::template fetch<D>(slot + (i % STAGES) * R::BYTES, src + (h0 + i) * sh, runs, on);
+    rows_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  const bool norm = kind < 2 && p.w[0] != nullptr;
+  float2 w[8], cs[4], sn[4];
+  if (on && kind < 2) {
+    if (norm) load_weights<T>(p.w[kind], runs, w);
+    angles<INTER>(runs, p.pos + b * p.pos_sb + n, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, cs, sn);
+  }
+  for (int i = 0; h0 + i < h1; ++i) {
+    rows_wait<STAGES - 2>();
+    float2 f[8];
+    R::read(slot + (i % STAGES) * R::BYTES, f);
+    fetch(i + STAGES - 1);  // into the slot of row i - 1
+    if (norm) {
+      float2 sq = mul2(f[0], f[0]);
+#pragma unroll
+      for (int e = 1; e < 8; ++e) sq = fma2(f[e], f[e], sq);
+      const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2(r, w[e]));
     }
-    T* dst;
-    if (kind == 0) {
-      dst = static_cast<T*>(p.out[0]) + ((b * p.Hq + hh) * p.N + n) * D;
-    } else if constexpr (PAGED) {
-      if (s_row[tt] < 0) continue;
-      dst = static_cast<T*>(kind == 1 ? p.kc : p.vc) + (s_row[tt] + int64_t(hh) * 16) * D;
-    } else {
-      dst = static_cast<T*>(p.out[1]) + ((b * p.Hkv + hh) * p.N + n) * D;
+    if (on) {
+      if (kind < 2) turn<INTER>(f, cs, sn);
+      store_row(dst + (h0 + i) * dh, runs, f);
     }
-    store8(dst + lo * 8, a);
-    store8(dst + hi * 8, bb);
   }
 }
 
-// Backward.  CTAs [0, ctas_q) walk the tokens' q rows, the others the k rows, so that a thread
-// keeps the 16 weight-gradient sums of its two pieces in registers over all its rows; the CTA's
-// sums go to `part`, which the second kernel adds up in a fixed order (no atomics: the same call
-// gives the same bits).
+// Backward.  CTAs [0, ctas_q) walk the units of q, the others those of k, so that a thread keeps
+// the 16 weight-gradient sums of its two pieces in registers over all its rows; the CTA's sums go
+// to `part`, which the second kernel adds up in a fixed order (no atomics: the same call gives
+// the same bits).
 template <typename T, typename TG, typename TO, int D, bool INTER>
-__global__ void __launch_bounds__(rope::THREADS) fa_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
+__global__ void __launch_bounds__(rope::THREADS, FA_ROPE_BWD_MINB) fa_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
   using namespace rope;
   using C = Cfg<D>;
-  __shared__ float s_cos[MAX_TOK][D / 2], s_sin[MAX_TOK][D / 2];
-  __shared__ float s_w[2][D / 2];
-  __shared__ float s_sum[THREADS / 32][D];
+  constexpr bool SPREAD = sizeof(T) + sizeof(TG) + sizeof(TO) > 6;  // any of them fp32
+  using RX = Slot<T, SPREAD>;
+  using RG = Slot<TG, SPREAD>;
+  extern __shared__ uint8_t rope_smem[];
+  const uint32_t slot_x = smem_u32(rope_smem) + RG::BYTES + threadIdx.x * RX::PIECE;
+  const uint32_t slot_g = smem_u32(rope_smem) + threadIdx.x * RG::PIECE;
   const int kind = int(blockIdx.x) < p.ctas_q ? 0 : 1;
-  const int64_t first_tile = kind ? blockIdx.x - p.ctas_q : blockIdx.x;
-  const int64_t n_cta = kind ? gridDim.x - p.ctas_q : p.ctas_q;
-  const int64_t tokens = int64_t(p.B) * p.N;
+  const int cta = kind ? blockIdx.x - p.ctas_q : blockIdx.x, n_cta = kind ? gridDim.x - p.ctas_q : p.ctas_q;
+  const int tokens = p.B * p.N;
   const bool norm = p.w[0] != nullptr;
-  const int heads = p.H[kind];
-  const T* x = static_cast<const T*>(p.x[kind]);
-  const TG* dy = static_cast<const TG*>(p.dy[kind]);
-  TO* dx = static_cast<TO*>(p.dx[kind]);
+  const int H = p.H[kind], chunks = p.chunks[kind];
+  const int64_t units = int64_t((tokens + C::TOKENS - 1) / C::TOKENS) * chunks;
+  const int lane = lane_id(), c = lane % C::L;
+  const Runs<D, SPREAD> runs(c < C::PAIRS ? c : 0, p.rd);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (norm) fill_weights<T, D>(s_w, p.w[kind], p.rd);
-  const int c = threadIdx.x % C::L;
-  const bool lane_on = c < C::PAIRS;
-  int lo, hi;
-  pieces<D>(c, p.rd, lo, hi);
-  const int first = threadIdx.x / C::L;
-  const int warp_first = (threadIdx.x & ~31) / C::L;
-  float sa[8], sb[8];  // weight-gradient sums of the two pieces
+  float2 w[8], sum[8];  // weights, and their gradients' sums
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sa[e] = sb[e] = 0.f;
+  for (int e = 0; e < 8; ++e) sum[e] = both(0.f);
+  if (norm) load_weights<T>(p.w[kind], runs, w);
 
-  for (int64_t t0 = first_tile * p.tok; t0 < tokens; t0 += n_cta * p.tok) {
-    const int nt = int(min(int64_t(p.tok), tokens - t0));
-    __syncthreads();  // the last tile's readers are done with the tables
-    for (int i = threadIdx.x; i < nt * (D / 2); i += THREADS) {
-      const int tt = i / (D / 2), j = i % (D / 2);
-      const int64_t t = t0 + tt;
-      float cc, ss;
-      angle<D, INTER>(j, p.pos + (t / p.N) * p.pos_sb + t % p.N, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, cc, ss);
-      s_cos[tt][slot<D>(j >> 3, j & 7)] = cc;
-      s_sin[tt][slot<D>(j >> 3, j & 7)] = -ss;
+  for (int64_t unit = int64_t(cta) * (THREADS / 32) + warp_id(); unit < units; unit += int64_t(n_cta) * (THREADS / 32)) {
+    const int tg = int(unit / chunks), h0 = int(unit - int64_t(tg) * chunks) * p.chunk, h1 = min(H, h0 + p.chunk);
+    const int t = tg * C::TOKENS + lane / C::L;
+    const bool on = c < C::PAIRS && t < tokens;
+    const int b = on ? t / p.N : 0, n = on ? t - b * p.N : 0;
+    const TG* dy = static_cast<const TG*>(p.dy[kind]) + (int64_t(b) * H * p.N + n) * D;
+    const T* x = static_cast<const T*>(p.x[kind]) + b * p.sb[kind] + n * p.sn[kind];
+    TO* dx = static_cast<TO*>(p.dx[kind]) + b * p.dsb[kind] + n * p.dsn[kind];
+    const int64_t gh = int64_t(p.N) * D, xh = p.sh[kind], dh = p.dsh[kind];
+    auto fetch = [&](int i) {
+      if (h0 + i < h1) {
+        const int at = (i % BWD_STAGES) * (RX::BYTES + RG::BYTES);
+        RG::template fetch<D>(slot_g + at, dy + (h0 + i) * gh, runs, on);
+        if (norm) RX::template fetch<D>(slot_x + at, x + (h0 + i) * xh, runs, on);
+      }
+      rows_commit();
+    };
+    rows_wait<0>();
+#pragma unroll
+    for (int i = 0; i < BWD_STAGES - 1; ++i) fetch(i);
+    float2 cs[4], sn[4];
+    if (on) {
+      angles<INTER>(runs, p.pos + b * p.pos_sb + n, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, cs, sn);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sn[e] = neg2(sn[e]);
     }
-    __syncthreads();
-    const int rows = nt * heads;
-    for (int base = 0; base + warp_first < rows; base += C::GROUPS) {
-      const int row = base + first;
-      const int tt = row / heads, h = row - tt * heads;
-      const bool on = lane_on && row < rows;
-      const int64_t t = t0 + tt, b = t / p.N, n = t % p.N;
-      Raw<T> rxa, rxb;
-      Raw<TG> rga, rgb;
-      rxa.clear();
-      rxb.clear();
-      rga.clear();
-      rgb.clear();
-      if (on) {
-        const TG* g = dy + ((b * heads + h) * p.N + n) * D;
-        rga.load(g + lo * 8);
-        rgb.load(g + hi * 8);
-        if (norm) {
-          const T* xs = x + b * p.sb[kind] + h * p.sh[kind] + n * p.sn[kind];
-          rxa.load(xs + lo * 8);
-          rxb.load(xs + hi * 8);
-        }
-      }
-      float ga[8], gb[8], cs[8], sn[8];
-      rga.get(ga);
-      rgb.get(gb);
-      if (on) {
-        read8<D>(s_cos[tt], c, cs);
-        read8<D>(s_sin[tt], c, sn);
-        turn<INTER>(ga, gb, cs, sn);
-      }
+    for (int i = 0; h0 + i < h1; ++i) {
+      rows_wait<BWD_STAGES - 2>();
+      const int at = (i % BWD_STAGES) * (RX::BYTES + RG::BYTES);
+      float2 g[8];
+      RG::read(slot_g + at, g);
+      if (on) turn<INTER>(g, cs, sn);
       if (norm) {
-        float xa[8], xb[8];
-        rxa.get(xa);
-        rxb.get(xb);
-        float sq = 0.f;
+        float2 xn[8];
+        RX::read(slot_x + at, xn);
+        fetch(i + BWD_STAGES - 1);  // into the slot of row i - 1
+        float2 sq = mul2(xn[0], xn[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq += xa[e] * xa[e] + xb[e] * xb[e];
-        sq = row_sum<C::L>(sq);
-        const float r = rsqrtf(sq * (1.f / D) + p.eps);
-        float wa[8], wb[8];
-        if (lane_on) {
-          read8<D>(s_w[0], c, wa);
-          read8<D>(s_w[1], c, wb);
-        }
-        float dot = 0.f;
+        for (int e = 1; e < 8; ++e) sq = fma2(xn[e], xn[e], sq);
+        const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
+        float2 dot2 = both(0.f);
+        if (on) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xa[e] *= r;  // n
-          xb[e] *= r;
-          if (on) {
-            sa[e] += ga[e] * xa[e];
-            sb[e] += gb[e] * xb[e];
-            ga[e] *= wa[e];  // h
-            gb[e] *= wb[e];
-            dot += ga[e] * xa[e] + gb[e] * xb[e];
+          for (int e = 0; e < 8; ++e) {
+            xn[e] = mul2(xn[e], r);  // n
+            sum[e] = fma2(g[e], xn[e], sum[e]);
+            g[e] = mul2(g[e], w[e]);  // h
+            dot2 = fma2(g[e], xn[e], dot2);
           }
         }
-        dot = row_sum<C::L>(dot) * (1.f / D);
+        const float2 dot = both(-row_sum<C::L>(dot2.x + dot2.y) * (1.f / D));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ga[e] = r * (ga[e] - xa[e] * dot);
-          gb[e] = r * (gb[e] - xb[e] * dot);
-        }
+        for (int e = 0; e < 8; ++e) g[e] = mul2(r, fma2(xn[e], dot, g[e]));
+      } else {
+        fetch(i + BWD_STAGES - 1);
       }
-      if (on) {
-        TO* dst = dx + b * p.dsb[kind] + h * p.dsh[kind] + n * p.dsn[kind];
-        store8(dst + lo * 8, ga);
-        store8(dst + hi * 8, gb);
-      }
+      if (on) store_row(dx + (h0 + i) * dh, runs, g);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!norm) return;
   // rows of a warp, then the warps
+  float* s_sum = reinterpret_cast<float*>(rope_smem);  // [warps][D], over the slots
+  rows_wait<0>();
+  __syncthreads();
 #pragma unroll
-  for (int m = C::L; m < 32; m <<= 1)
+  for (int e = 0; e < 8; ++e) {
+    float2 v = sum[e];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      sa[e] += __shfl_xor_sync(0xffffffffu, sa[e], m);
-      sb[e] += __shfl_xor_sync(0xffffffffu, sb[e], m);
+    for (int m = C::L; m < 32; m <<= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
     }
-  if (lane_id() < C::L && lane_on) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s_sum[warp_id()][lo * 8 + e] = sa[e];
-      s_sum[warp_id()][hi * 8 + e] = sb[e];
-    }
+    if (lane < C::PAIRS) *reinterpret_cast<float2*>(&s_sum[warp_id() * D + runs.q[e >> 1] * 4 + 2 * (e & 1)]) = v;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += THREADS) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) v += s_sum[w][i];
+    for (int w = 0; w < THREADS / 32; ++w) v += s_sum[w * D + i];
     p.part[int64_t(blockIdx.x) * D + i] = v;
   }
 }
 
-// dw of q (block 0) and k (block 1): the CTAs' partial sums, eight strands per column.
-__global__ void __launch_bounds__(256) fa_qk_norm_rope_dw_kernel(const float* part, float* dwq, float* dwk, int D,
+// dw of q (blockIdx.y 0) and k (1), 8 columns a CTA: 64 strands per column add the CTAs' partial
+// sums, then the strands are added pairwise (one CTA per 32 columns with 8 strands took 9 to 29 us).
+__global__ void __launch_bounds__(512) fa_qk_norm_rope_dw_kernel(const float* part, float* dwq, float* dwk, int D,
                                                                  int ctas_q, int ctas) {
-  __shared__ float s[256];
+  __shared__ float s[512];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r0 = blockIdx.x ? ctas_q : 0, r1 = blockIdx.x ? ctas : ctas_q;
-  float* dw = blockIdx.x ? dwk : dwq;
-  const int col = threadIdx.x & 31, strand = threadIdx.x >> 5;
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    float v = 0.f;
-    for (int r = r0 + strand; r < r1; r += 8) v += part[int64_t(r) * D + c0 + col];
-    s[threadIdx.x] = v;
+  const int r0 = blockIdx.y ? ctas_q : 0, r1 = blockIdx.y ? ctas : ctas_q;
+  const int col = blockIdx.x * 8 + (threadIdx.x & 7), strand = threadIdx.x >> 3;
+  float v = 0.f;
+#pragma unroll 4
+  for (int r = r0 + strand; r < r1; r += 64) v += part[int64_t(r) * D + col];
+  s[threadIdx.x] = v;
+  for (int k = 256; k >= 8; k >>= 1) {
     __syncthreads();
-    if (strand == 0) {
-      for (int k = 1; k < 8; ++k) v += s[k * 32 + col];
-      dw[c0 + col] = v;
-    }
-    __syncthreads();
+    if (int(threadIdx.x) < k) s[threadIdx.x] += s[threadIdx.x + k];
   }
+  if (threadIdx.x < 8) (blockIdx.y ? dwk : dwq)[col] = s[threadIdx.x];
 }
 
 }  // namespace fa
