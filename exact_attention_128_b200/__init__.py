@@ -32,6 +32,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -71,8 +72,6 @@ _DT = {torch.float32: FA_DTYPE_F32, torch.bfloat16: FA_DTYPE_BF16}
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _i64 = ctypes.c_int64
-_i64x3 = ctypes.POINTER(ctypes.c_int64 * 3)
-_ix3 = ctypes.POINTER(ctypes.c_int * 3)
 
 # name -> (restype, argtypes); the same names as the C entry points
 EXPORTED = {
@@ -86,24 +85,31 @@ EXPORTED = {
     "fa_paged_decode_noalloc": (_i, [_vp] * 7 + [_i] * 7 + [_f, _i, _vp]),
     "fa_paged_kv_append": (_i, [_vp] * 6 + [_i] * 6 + [_i, _vp]),
     "fa_paged_prefill": (_i, [_vp] * 6 + [_vp, _vp] + [_i] * 8 + [_f, _i, _i, _vp]),
-    "fa_qk_norm_rope": (_i, [_vp] * 2 + [_i64x3] * 2 + [_vp] * 3 + [_i64] * 2 + [_vp] * 3 + [_i] * 6 + [_ix3]
-                        + [_i] * 2 + [_f, _i, _vp]),
-    "fa_qk_norm_rope_append": (_i, [_vp] * 3 + [_i64x3] * 3 + [_vp] * 3 + [_i64] * 2 + [_vp] * 7 + [_i] * 9 + [_ix3]
-                               + [_i] * 2 + [_f, _i, _vp]),
+    # (arguments in one struct, passed as its bytes, and the stream)
+    "fa_qk_norm_rope": (_i, [_vp, _vp]),
+    "fa_qk_norm_rope_append": (_i, [_vp, _vp]),
     "fa_qk_norm_rope_bwd_workspace_size": (_sz, [_i]),
-    "fa_qk_norm_rope_bwd": (_i, [_vp] * 2 + [_i] + [_vp] * 2 + [_i64x3] * 2 + [_vp] * 3 + [_i64] * 2 + [_vp] * 3
-                            + [_i64x3] * 2 + [_i] + [_vp] * 2 + [_i] * 6 + [_ix3] + [_i] * 2 + [_f, _i]
-                            + [_vp, _sz, _vp]),
+    "fa_qk_norm_rope_bwd": (_i, [_vp, _vp]),
     "fa_paged_decode_shared_workspace_size": (_sz, [_i] * 7),
-    "fa_paged_decode_shared": (_i, [_vp] * 9 + [_i] * 8 + [_f, _i, _vp, _sz, _vp]),
+    "fa_paged_decode_shared": (_i, [_vp, _vp]),
     "fa_paged_decode_scored_workspace_size": (_sz, [_i] * 6),
-    "fa_paged_decode_scored": (_i, [_vp] * 8 + [_i] * 7 + [_f, _i, _vp, _sz, _vp]),
+    "fa_paged_decode_scored": (_i, [_vp, _vp]),
     "fa_paged_evict_workspace_size": (_sz, [_i] * 4),
-    "fa_paged_evict": (_i, [_vp] * 10 + [_i] * 8 + [_i, _vp, _sz, _vp]),
+    "fa_paged_evict": (_i, [_vp, _vp]),
     "fa_device_status": (_i, [_i]),
     "fa_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "fa_selftest_wait_timeout": (_i, [_vp]),
     "fa_set_decode_split": (_i, [_i]),
+}
+
+# name -> packer of its argument struct: pointers and sizes, int64 strides, ints, eps or scale, ints
+PACKED = {
+    "fa_qk_norm_rope": struct.Struct("8P8q11ifi").pack,
+    "fa_qk_norm_rope_append": struct.Struct("13P11q14ifi").pack,
+    "fa_qk_norm_rope_bwd": struct.Struct("14P14q11if3i").pack,
+    "fa_paged_decode_shared": struct.Struct("11P8ifi").pack,
+    "fa_paged_decode_scored": struct.Struct("10P7ifi").pack,
+    "fa_paged_evict": struct.Struct("12P9i").pack,
 }
 
 
@@ -293,50 +299,64 @@ def paged_prefill(q, k_cache, v_cache, block_table, ctx_lens, q_lens, causal: bo
 # not be the current one; the call runs on that device's current stream.
 # ------------------------------------------------------------------------------------
 def _expect(name, t, shape, dtype, device):
-    """A contiguous tensor of this shape and type on this device; its address."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+    """Address of a contiguous tensor of this shape and type on the CUDA device of this index."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on device {device}, got "
+                     f"{_described(t)}")
 
 
-def _call(fn, device, *args):
-    """Run one entry point on `device` and its current stream (appended as the last argument)."""
-    L = _lib or lib()
-    index = device.index
-    if index == torch.cuda.current_device():
-        st = getattr(L, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
+def _described(t):
+    if not isinstance(t, torch.Tensor):
+        return type(t).__name__
+    return f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}"
+
+
+def _device(name, t, dim):
+    """Index of the CUDA device of the tensor that a call's others are held against."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dim:
+        raise ValueError(f"{name} must be a CUDA tensor of {dim} dimensions, got {_described(t)}")
+    return t.get_device()
+
+
+def _call(name, device, *args):
+    """Run one entry point on the device of this index and its current stream."""
+    fn, packed = getattr(_lib, name), PACKED[name](*args)
+    if device == torch._C._cuda_getDevice():
+        st = fn(packed, torch._C._cuda_getCurrentRawStream(device))
     else:
-        with torch.cuda.device(index):
-            st = getattr(L, fn)(*args, torch._C._cuda_getCurrentRawStream(index))
-    if st != FA_OK:
-        raise FAError(fn, st)
+        with torch.cuda.device(device):
+            st = fn(packed, torch._C._cuda_getCurrentRawStream(device))
+    if st:
+        raise FAError(name, st)
 
 
-def _workspace(workspace, need, device):
-    """(address, bytes) of the caller's workspace, or of a new one (third item keeps it alive)."""
+def _workspace(workspace, need, like):
+    """(address, bytes) of the caller's workspace, or of a new one; the last item keeps it alive."""
     if workspace is None:
-        workspace = torch.empty(max(need, 1), device=device, dtype=torch.uint8)
-    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        workspace = like.new_empty(need or 1, dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}, got {_described(workspace)}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _rows(name, t, dtype, device, shape=None):
+def _rows(name, t, dtype, device, shape):
     """Address and {batch, head, token} strides of a [B,H,N,d] view whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4 or t.dtype != dtype or t.device != device or (shape is not None and t.shape != shape):
-        want = "[B,H,N,d]" if shape is None else tuple(shape)
-        raise ValueError(f"{name} must be {dtype} {want} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    B, H, N, d = t.shape
-    sb, sh, sn, sd = t.stride()
-    if sd != 1 and d > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    # a dimension of size 1 has no stride of its own
-    return t.data_ptr(), (ctypes.c_int64 * 3)(sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device:
+            sb, sh, sn, sd = t.stride()
+            if sd == 1 or shape[3] == 1:
+                # a dimension of size 1 has no stride of its own
+                return t.data_ptr(), (sb if shape[0] > 1 else 0, sh if shape[1] > 1 else 0,
+                                      sn if shape[2] > 1 else 0)
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)} with a contiguous last dimension on device {device}, got "
+                     f"{_described(t)}")
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
@@ -347,45 +367,54 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
     return torch.exp(i * (-2.0 * math.log(base) / rotary_dim))
 
 
-def _rope_args(q, positions, inv_freq, sections, B, N):
+_ZEROS = {1: (0, 0), 2: (0,), 3: ()}
+
+
+def _rope_args(device, positions, inv_freq, sections, B, N):
     """Rotary arguments in their C form: position pointer and strides, frequencies, sections."""
-    device = q.device
-    if not isinstance(positions, torch.Tensor) or not positions.is_cuda:
-        raise ValueError("positions must be a CUDA tensor")
-    if positions.dtype != torch.int32 or positions.device != device or positions.dim() not in (1, 2, 3):
-        raise ValueError(f"positions must be int32 [N], [B,N] or [axes,B,N] on {device}")
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be a tensor [rotary_dim / 2]")
-    half = inv_freq.shape[0]
+    try:
+        half = inv_freq.shape[0]
+        shape = positions.shape
+        dims = len(shape)
+    except (AttributeError, IndexError):
+        raise ValueError(f"inv_freq must be a tensor [rotary_dim / 2], positions one of [N], [B,N] or [axes,B,N], got "
+                         f"{_described(inv_freq)} and {_described(positions)}") from None
     freq = _expect("inv_freq", inv_freq, (half,), torch.float64, device)
-    axes = positions.shape[0] if positions.dim() == 3 else 1
-    if sections is None:
-        sections = (half,)
-    if len(sections) != axes or not 1 <= axes <= 3 or sum(sections) != half:
+    axes = shape[0] if dims == 3 else 1
+    sec = (half,) if sections is None else tuple(sections)
+    if len(sec) != axes or not 1 <= axes <= 3 or sum(sec) != half:
         raise ValueError(f"{axes} axes of positions need {axes} sections (1 to 3) that sum to {half}, got {sections}")
-    want = {1: (N,), 2: (B, N), 3: (axes, B, N)}[positions.dim()]
-    if positions.shape != want or (N > 1 and positions.stride(-1) != 1):
-        raise ValueError(f"positions must be {want} with a contiguous last dimension, got {tuple(positions.shape)} with "
-                         f"strides {positions.stride()}")
-    sa = positions.stride(0) if axes > 1 else 0
-    sb = positions.stride(-2) if positions.dim() > 1 and B > 1 else 0
-    return positions.data_ptr(), sa, sb, freq, 2 * half, (ctypes.c_int * 3)(*sections), axes
+    if shape != ((axes, B, N) if dims == 3 else (B, N) if dims == 2 else (N,)):
+        raise ValueError(f"positions must be [N], [B,N] or [axes,B,N] with B = {B} and N = {N}, got {tuple(shape)}")
+    strides = positions.stride()
+    if positions.dtype is not torch.int32 or positions.get_device() != device or (N > 1 and strides[-1] != 1):
+        raise ValueError(f"positions must be int32 on device {device} with a contiguous last dimension, got "
+                         f"{_described(positions)}")
+    return (positions.data_ptr(), strides[0] if axes > 1 else 0, strides[-2] if dims > 1 and B > 1 else 0, freq,
+            2 * half, sec + _ZEROS[axes], axes)
 
 
 def _rope_weights(q_weight, k_weight, d, dtype, device):
-    if (q_weight is None) != (k_weight is None):
+    if q_weight is None and k_weight is None:
+        return 0, 0
+    if q_weight is None or k_weight is None:
         raise ValueError("q_weight and k_weight come together, or neither")
-    if q_weight is None:
-        return None, None
     return _expect("q_weight", q_weight, (d,), dtype, device), _expect("k_weight", k_weight, (d,), dtype, device)
 
 
-def _like_rows(t, dtype):
-    """An empty [B,H,N,d] tensor of `dtype` whose rows lie in the order of t's (a fused projection's
-    view gives [B,N,H,d] memory)."""
-    order = sorted(range(3), key=lambda i: (-t.stride(i) if t.shape[i] > 1 else 0, i))
-    out = torch.empty([t.shape[i] for i in order] + [t.shape[3]], device=t.device, dtype=dtype)
-    return out.permute([order.index(i) for i in range(3)] + [3])
+def _heads(name, t):
+    """Size of dimension 1 of a [B,H,N,d] tensor or cache."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA tensor of 4 dimensions, got {_described(t)}")
+    return t.shape[1]
+
+
+def _like_rows(t, B, H, N, d, dtype):
+    """An empty [B,H,N,d] tensor: as [B,N,H,d] in memory where t is a view of a projection, else contiguous."""
+    strides = t.stride()
+    if strides[2] > strides[1]:
+        return t.new_empty((B, N, H, d), dtype=dtype).transpose(1, 2)
+    return t.new_empty((B, H, N, d), dtype=dtype)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections=None, interleaved: bool = False,
@@ -394,25 +423,25 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections=None, i
     of a fused projection) -> contiguous (q', k') for fwd.  Weights [d], or None for both: the
     rotation alone.  positions int32 [N], [B,N] or [axes,B,N] with one section per axis;
     inv_freq float64 [rotary_dim / 2] (see rope_frequencies)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("expected q [B,Hq,N,d] and k [B,Hkv,N,d]")
-    B, Hq, N, d = q.shape
-    device, dtype = q.device, q.dtype
-    qp, qs = _rows("q", q, dtype, device)
-    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-    kp, ks = _rows("k", k, dtype, device, (B, Hkv, N, d))
+    device = _device("q", q, 4)
+    B, Hq, N, d = shape = q.shape
+    dtype, Hkv = q.dtype, _heads("k", k)
+    kshape = (B, Hkv, N, d)
+    qp, qs = _rows("q", q, dtype, device, shape)
+    kp, ks = _rows("k", k, dtype, device, kshape)
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}")
-    pos, sa, sb, freq, rd, sec, axes = _rope_args(q, positions, inv_freq, sections, B, N)
+    pos, sa, sb, freq, rd, sec, axes = _rope_args(device, positions, inv_freq, sections, B, N)
     wq, wk = _rope_weights(q_weight, k_weight, d, dtype, device)
     if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), device=device, dtype=dtype)
+        q_out = q.new_empty(shape)
     if k_out is None:
-        k_out = torch.empty((B, Hkv, N, d), device=device, dtype=dtype)
-    qo = _expect("q_out", q_out, (B, Hq, N, d), dtype, device)
-    ko = _expect("k_out", k_out, (B, Hkv, N, d), dtype, device)
-    _call("fa_qk_norm_rope", device, qp, kp, qs, ks, wq, wk, pos, sa, sb, freq, qo, ko, B, Hq, Hkv, N, d, rd, sec, axes,
-          int(bool(interleaved)), eps, _DT[dtype])
+        k_out = k.new_empty(kshape)
+    qo = _expect("q_out", q_out, shape, dtype, device)
+    ko = _expect("k_out", k_out, kshape, dtype, device)
+    lib()
+    _call("fa_qk_norm_rope", device, qp, kp, wq, wk, pos, freq, qo, ko, *qs, *ks, sa, sb, B, Hq, Hkv, N, d, rd, *sec,
+          axes, 1 if interleaved else 0, eps, _DT[dtype])
     return q_out, k_out
 
 
@@ -420,36 +449,40 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_fr
                      interleaved: bool = False, eps: float = 1e-6, grad_dtype: torch.dtype | None = None, dq=None,
                      dk=None, workspace=None):
     """Gradients of qk_norm_rope: (dq, dk, dq_weight, dk_weight) from dq_out, dk_out (contiguous, as
-    bwd returns them).  dq and dk have grad_dtype (default: q's) and lie in memory as q and k do,
-    or are the [B,H,N,d] views given; the weight gradients are fp32 [d] (None without weights)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("expected q [B,Hq,N,d] and k [B,Hkv,N,d]")
-    B, Hq, N, d = q.shape
-    device, dtype = q.device, q.dtype
-    qp, qs = _rows("q", q, dtype, device)
-    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-    kp, ks = _rows("k", k, dtype, device, (B, Hkv, N, d))
-    grad_dtype = dtype if grad_dtype is None else grad_dtype
-    if dtype not in _DT or grad_dtype not in _DT or not isinstance(dq_out, torch.Tensor) or dq_out.dtype not in _DT:
-        raise ValueError(f"unsupported dtypes: {dtype} with gradients {getattr(dq_out, 'dtype', None)} -> {grad_dtype}")
-    dqo = _expect("dq_out", dq_out, (B, Hq, N, d), dq_out.dtype, device)
-    dko = _expect("dk_out", dk_out, (B, Hkv, N, d), dq_out.dtype, device)
-    pos, sa, sb, freq, rd, sec, axes = _rope_args(q, positions, inv_freq, sections, B, N)
+    bwd returns them).  dq and dk have grad_dtype (default: q's) and lie in memory as q and k do (a
+    projection's [B,N,H,d], or contiguous), or are the [B,H,N,d] views given; the weight gradients
+    are fp32 [d] (None without weights)."""
+    device = _device("q", q, 4)
+    B, Hq, N, d = shape = q.shape
+    dtype, Hkv = q.dtype, _heads("k", k)
+    kshape = (B, Hkv, N, d)
+    qp, qs = _rows("q", q, dtype, device, shape)
+    kp, ks = _rows("k", k, dtype, device, kshape)
+    if grad_dtype is None:
+        grad_dtype = dtype
+    dout_dtype = dq_out.dtype if isinstance(dq_out, torch.Tensor) else None
+    if dtype not in _DT or grad_dtype not in _DT or dout_dtype not in _DT:
+        raise ValueError(f"unsupported dtypes: {dtype} with gradients {dout_dtype} -> {grad_dtype}")
+    dqo = _expect("dq_out", dq_out, shape, dout_dtype, device)
+    dko = _expect("dk_out", dk_out, kshape, dout_dtype, device)
+    pos, sa, sb, freq, rd, sec, axes = _rope_args(device, positions, inv_freq, sections, B, N)
     wq, wk = _rope_weights(q_weight, k_weight, d, dtype, device)
     if dq is None:
-        dq = _like_rows(q, grad_dtype)
+        dq = _like_rows(q, B, Hq, N, d, grad_dtype)
     if dk is None:
-        dk = _like_rows(k, grad_dtype)
-    dqp, dqs = _rows("dq", dq, grad_dtype, device, (B, Hq, N, d))
-    dkp, dks = _rows("dk", dk, grad_dtype, device, (B, Hkv, N, d))
-    dwq = dwk = None
-    ws, ws_bytes, keep = None, 0, None
-    if wq is not None:
-        dwq, dwk = torch.empty((2, d), device=device, dtype=torch.float32).unbind(0)
-        ws, ws_bytes, keep = _workspace(workspace, lib().fa_qk_norm_rope_bwd_workspace_size(d), device)
-    _call("fa_qk_norm_rope_bwd", device, dqo, dko, _DT[dq_out.dtype], qp, kp, qs, ks, wq, wk, pos, sa, sb, freq, dqp, dkp,
-          dqs, dks, _DT[grad_dtype], None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), B,
-          Hq, Hkv, N, d, rd, sec, axes, int(bool(interleaved)), eps, _DT[dtype], ws, ws_bytes)
+        dk = _like_rows(k, B, Hkv, N, d, grad_dtype)
+    dqp, dqs = _rows("dq", dq, grad_dtype, device, shape)
+    dkp, dks = _rows("dk", dk, grad_dtype, device, kshape)
+    dwq = dwk = keep = None
+    dwqp = dwkp = ws = ws_bytes = 0
+    L = lib()
+    if wq:
+        dwq, dwk = q.new_empty(d, dtype=torch.float32), q.new_empty(d, dtype=torch.float32)
+        dwqp, dwkp = dwq.data_ptr(), dwk.data_ptr()
+        ws, ws_bytes, keep = _workspace(workspace, L.fa_qk_norm_rope_bwd_workspace_size(d), q)
+    _call("fa_qk_norm_rope_bwd", device, dqo, dko, qp, kp, wq, wk, pos, freq, dqp, dkp, dwqp, dwkp, ws, ws_bytes, *qs,
+          *ks, *dqs, *dks, sa, sb, B, Hq, Hkv, N, d, rd, *sec, axes, 1 if interleaved else 0, eps, _DT[dtype],
+          _DT[dout_dtype], _DT[grad_dtype])
     return dq, dk, dwq, dwk
 
 
@@ -459,34 +492,38 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_cach
     views) with k' and v written into the paged caches: token i of request r at cache position
     ctx_lens[r] - q_lens[r] + i.  Returns q' [R,Hq,Nq_max,d], whose rows i >= q_lens[r] are left as
     q_out holds them (undefined where q_out is None)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("expected q [R,Hq,Nq_max,d] and k, v [R,Hkv,Nq_max,d]")
-    R, Hq, N, d = q.shape
-    device, bf16 = q.device, torch.bfloat16
-    qp, qs = _rows("q", q, bf16, device)
-    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-    kp, ks = _rows("k", k, bf16, device, (R, Hkv, N, d))
-    vp, vs = _rows("v", v, bf16, device, (R, Hkv, N, d))
-    pos, sa, sb, freq, rd, sec, axes = _rope_args(q, positions, inv_freq, sections, R, N)
+    device = _device("q", q, 4)
+    R, Hq, N, d = shape = q.shape
+    Hkv, bf16 = _heads("k", k), torch.bfloat16
+    kshape = (R, Hkv, N, d)
+    qp, qs = _rows("q", q, bf16, device, shape)
+    kp, ks = _rows("k", k, bf16, device, kshape)
+    vp, vs = _rows("v", v, bf16, device, kshape)
+    pos, sa, sb, freq, rd, sec, axes = _rope_args(device, positions, inv_freq, sections, R, N)
     wq, wk = _rope_weights(q_weight, k_weight, d, bf16, device)
     num_blocks, bs, maxb, kc, vc, bt, ctx = _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device)
     ql = _expect("q_lens", q_lens, (R,), torch.int32, device)
     if q_out is None:
-        q_out = torch.empty((R, Hq, N, d), device=device, dtype=bf16)
-    qo = _expect("q_out", q_out, (R, Hq, N, d), bf16, device)
-    _call("fa_qk_norm_rope_append", device, qp, kp, vp, qs, ks, vs, wq, wk, pos, sa, sb, freq, kc, vc, bt, ctx, ql, qo, R,
-          Hq, Hkv, N, d, bs, maxb, num_blocks, rd, sec, axes, int(bool(interleaved)), eps, FA_DTYPE_BF16)
+        q_out = q.new_empty(shape)
+    qo = _expect("q_out", q_out, shape, bf16, device)
+    lib()
+    _call("fa_qk_norm_rope_append", device, qp, kp, vp, wq, wk, pos, freq, kc, vc, bt, ctx, ql, qo, *qs, *ks, *vs, sa, sb,
+          R, Hq, Hkv, N, d, bs, maxb, num_blocks, rd, *sec, axes, 1 if interleaved else 0, eps, FA_DTYPE_BF16)
     return q_out
 
 
 def _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device):
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("caches must be [num_blocks,Hkv,block_size,d]")
-    num_blocks, bs = k_cache.shape[0], k_cache.shape[2]
-    shape = (num_blocks, Hkv, bs, d)
+    try:
+        shape = k_cache.shape
+        num_blocks, _, bs, _ = shape
+        maxb = block_table.shape[1]
+    except (AttributeError, ValueError, IndexError):
+        raise ValueError(f"caches must be [num_blocks,Hkv,block_size,d] and block_table [R,max_blocks], got "
+                         f"{_described(k_cache)} and {_described(block_table)}") from None
+    if shape[1] != Hkv or shape[3] != d:
+        raise ValueError(f"caches must be [num_blocks,{Hkv},block_size,{d}], got {_described(k_cache)}")
     kc = _expect("k_cache", k_cache, shape, torch.bfloat16, device)
     vc = _expect("v_cache", v_cache, shape, torch.bfloat16, device)
-    maxb = block_table.shape[1] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
     bt = _expect("block_table", block_table, (R, maxb), torch.int32, device)
     return num_blocks, bs, maxb, kc, vc, bt, _expect("ctx_lens", ctx_lens, (R,), torch.int32, device)
 
@@ -496,38 +533,36 @@ def paged_decode_shared_workspace_size(R, Hq, Hkv, d, max_prefix_blocks, max_blo
                                                            block_size))
 
 
+def _decode_outputs(q, shape, device, with_lse, out):
+    if out is None:
+        out = q.new_empty(shape)
+    op = _expect("out", out, shape, torch.bfloat16, device)
+    if not with_lse:
+        return out, None, op, 0
+    lse = q.new_empty(shape[:2], dtype=torch.float32)
+    return out, lse, op, lse.data_ptr()
+
+
 def paged_decode_shared(q, k_cache, v_cache, prefix_table, prefix_len, block_table, ctx_lens,
                         scale: float | None = None, with_lse: bool = True, workspace=None, out=None):
     """One decode step of R requests behind a common prefix, which is computed once for all:
     prefix_table [max_prefix_blocks] and prefix_len [1] (device, int32) name its tokens, block_table
     and ctx_lens each request's own ones; either length may be 0 -> (o [R,Hq,d], lse [R,Hq])."""
-    o, lse, R, Hq, Hkv, d, head, mid = _decode_args(q, k_cache, v_cache, block_table, ctx_lens, scale, with_lse, out)
-    device = q.device
-    num_blocks, bs, maxb, scale = mid
-    pb = prefix_table.shape[0] if isinstance(prefix_table, torch.Tensor) and prefix_table.dim() == 1 else 0
-    pt = _expect("prefix_table", prefix_table, (pb,), torch.int32, device)
-    pl = _expect("prefix_len", prefix_len, (1,), torch.int32, device)
-    need = lib().fa_paged_decode_shared_workspace_size(R, Hq, Hkv, d, pb, maxb, bs)
-    ws, ws_bytes, keep = _workspace(workspace, need, device)
-    _call("fa_paged_decode_shared", device, *head[:3], pt, pl, *head[3:], o.data_ptr(),
-          None if lse is None else lse.data_ptr(), R, Hq, Hkv, d, bs, pb, maxb, num_blocks, scale, FA_DTYPE_BF16, ws,
-          ws_bytes)
-    return o, lse
-
-
-def _decode_args(q, k_cache, v_cache, block_table, ctx_lens, scale, with_lse, out):
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("expected q [R,Hq,d]")
-    R, Hq, d = q.shape
-    device = q.device
-    Hkv = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
-    qp = _expect("q", q, (R, Hq, d), torch.bfloat16, device)
+    device = _device("q", q, 3)
+    R, Hq, d = shape = q.shape
+    Hkv, i32 = _heads("k_cache", k_cache), torch.int32
+    qp = _expect("q", q, shape, torch.bfloat16, device)
     num_blocks, bs, maxb, kc, vc, bt, ctx = _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device)
-    if out is None:
-        out = torch.empty((R, Hq, d), device=device, dtype=torch.bfloat16)
-    _expect("out", out, (R, Hq, d), torch.bfloat16, device)
-    lse = torch.empty((R, Hq), device=device, dtype=torch.float32) if with_lse else None
-    return out, lse, R, Hq, Hkv, d, (qp, kc, vc, bt, ctx), (num_blocks, bs, maxb, d ** -0.5 if scale is None else scale)
+    pb = prefix_table.shape[0] if isinstance(prefix_table, torch.Tensor) and prefix_table.dim() == 1 else 0
+    pt = _expect("prefix_table", prefix_table, (pb,), i32, device)
+    pl = _expect("prefix_len", prefix_len, (1,), i32, device)
+    L = lib()
+    need = L.fa_paged_decode_shared_workspace_size(R, Hq, Hkv, d, pb, maxb, bs)
+    ws, ws_bytes, keep = _workspace(workspace, need, q)
+    o, lse, op, lp = _decode_outputs(q, shape, device, with_lse, out)
+    _call("fa_paged_decode_shared", device, qp, kc, vc, pt, pl, bt, ctx, op, lp, ws, ws_bytes, R, Hq, Hkv, d, bs, pb,
+          maxb, num_blocks, d ** -0.5 if scale is None else scale, FA_DTYPE_BF16)
+    return o, lse
 
 
 def paged_decode_scored_workspace_size(R, Hq, Hkv, d, max_blocks_per_seq, block_size) -> int:
@@ -538,14 +573,18 @@ def paged_decode_scored(q, k_cache, v_cache, block_table, ctx_lens, weights, sca
                         with_lse: bool = True, workspace=None, out=None):
     """A decode step that adds to weights [R,Hkv,max_blocks*16] (fp32, in place) the attention each
     cached token gets, summed over the query heads of its kv head -> (o [R,Hq,d], lse [R,Hq])."""
-    o, lse, R, Hq, Hkv, d, head, mid = _decode_args(q, k_cache, v_cache, block_table, ctx_lens, scale, with_lse, out)
-    device = q.device
-    num_blocks, bs, maxb, scale = mid
+    device = _device("q", q, 3)
+    R, Hq, d = shape = q.shape
+    Hkv = _heads("k_cache", k_cache)
+    qp = _expect("q", q, shape, torch.bfloat16, device)
+    num_blocks, bs, maxb, kc, vc, bt, ctx = _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device)
     w = _expect("weights", weights, (R, Hkv, maxb * bs), torch.float32, device)
-    need = lib().fa_paged_decode_scored_workspace_size(R, Hq, Hkv, d, maxb, bs)
-    ws, ws_bytes, keep = _workspace(workspace, need, device)
-    _call("fa_paged_decode_scored", device, *head, w, o.data_ptr(), None if lse is None else lse.data_ptr(), R, Hq, Hkv,
-          d, bs, maxb, num_blocks, scale, FA_DTYPE_BF16, ws, ws_bytes)
+    L = lib()
+    need = L.fa_paged_decode_scored_workspace_size(R, Hq, Hkv, d, maxb, bs)
+    ws, ws_bytes, keep = _workspace(workspace, need, q)
+    o, lse, op, lp = _decode_outputs(q, shape, device, with_lse, out)
+    _call("fa_paged_decode_scored", device, qp, kc, vc, bt, ctx, w, op, lp, ws, ws_bytes, R, Hq, Hkv, d, bs, maxb,
+          num_blocks, d ** -0.5 if scale is None else scale, FA_DTYPE_BF16)
     return o, lse
 
 
@@ -559,28 +598,27 @@ def paged_evict(k_cache, v_cache, block_table, ctx_lens, seq_lens, weights, slot
     others, `keep` in all: moves their rows in the caches and returns (new_ctx [R], weights,
     slot_pos) for the next steps.  seq_lens [R]: tokens of each sequence so far, evicted ones
     included; slot_pos int32 [R,Hkv,max_blocks*16]: -1 everywhere at the start."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("caches must be [num_blocks,Hkv,block_size,d]")
-    device, f32, i32 = k_cache.device, torch.float32, torch.int32
-    Hkv, d = k_cache.shape[1], k_cache.shape[3]
+    device = _device("k_cache", k_cache, 4)
+    _, Hkv, _, d = k_cache.shape
+    f32, i32 = torch.float32, torch.int32
     R = block_table.shape[0] if isinstance(block_table, torch.Tensor) and block_table.dim() == 2 else 0
     num_blocks, bs, maxb, kc, vc, bt, ctx = _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device)
     shape = (R, Hkv, maxb * bs)
     seq = _expect("seq_lens", seq_lens, (R,), i32, device)
     w, sp = _expect("weights", weights, shape, f32, device), _expect("slot_pos", slot_pos, shape, i32, device)
     if weights_out is None:
-        weights_out = torch.empty(shape, device=device, dtype=f32)
+        weights_out = torch.empty_like(weights)
     if slot_pos_out is None:
-        slot_pos_out = torch.empty(shape, device=device, dtype=i32)
+        slot_pos_out = torch.empty_like(slot_pos)
     if new_ctx is None:
-        new_ctx = torch.empty((R,), device=device, dtype=i32)
+        new_ctx = torch.empty_like(ctx_lens)
     wo = _expect("weights_out", weights_out, shape, f32, device)
     so = _expect("slot_pos_out", slot_pos_out, shape, i32, device)
     nc = _expect("new_ctx", new_ctx, (R,), i32, device)
-    need = lib().fa_paged_evict_workspace_size(R, Hkv, maxb, keep)
-    ws, ws_bytes, alive = _workspace(workspace, need, device)
-    _call("fa_paged_evict", device, kc, vc, bt, ctx, seq, w, sp, wo, so, nc, R, Hkv, d, bs, maxb, num_blocks, keep, recent,
-          FA_DTYPE_BF16, ws, ws_bytes)
+    L = lib()
+    ws, ws_bytes, alive = _workspace(workspace, L.fa_paged_evict_workspace_size(R, Hkv, maxb, keep), k_cache)
+    _call("fa_paged_evict", device, kc, vc, bt, ctx, seq, w, sp, wo, so, nc, ws, ws_bytes, R, Hkv, d, bs, maxb, num_blocks,
+          keep, recent, FA_DTYPE_BF16)
     return new_ctx, weights_out, slot_pos_out
 
 

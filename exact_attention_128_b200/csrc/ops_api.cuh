@@ -16,8 +16,8 @@ namespace {
 
 // Rotation arguments that every rotary entry point shares: sizes, then one of `out` launches.
 fa_status rope_check(const int* positions, const double* inv_freq, int B, int Hq, int Hkv, int N, int d, int rotary_dim,
-                     const int* sections, int n_axes, int interleaved, float eps, fa_dtype dtype) {
-  if (!positions || !inv_freq || !sections) return FA_ERR_INVALID_ARG;
+                     const int* sections, int n_axes, int interleaved, float eps, int dtype) {
+  if (!positions || !inv_freq) return FA_ERR_INVALID_ARG;
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0 || rotary_dim <= 0) return FA_ERR_INVALID_ARG;
   if (!aligned(positions, 4) || !aligned(inv_freq, 8)) return FA_ERR_INVALID_ARG;
   if (n_axes < 1 || n_axes > 3 || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
@@ -36,9 +36,9 @@ fa_status rope_check(const int* positions, const double* inv_freq, int B, int Hq
 }
 
 // Rows of 16-byte pieces at any (batch, head, token): base and strides (elements) are multiples of 16 bytes.
-bool rope_rows(const void* p, const int64_t* strides, fa_dtype dtype) {
+bool rope_rows(const void* p, const int64_t* strides, int dtype) {
   const int64_t per = dtype == FA_DTYPE_F32 ? 4 : 8;
-  if (!p || !strides || !aligned(p, 16)) return false;
+  if (!p || !aligned(p, 16)) return false;
   for (int i = 0; i < 3; ++i)
     if (strides[i] < 0 || strides[i] % per != 0) return false;
   return true;
@@ -98,7 +98,8 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
   if (launch_pdl(kern, dim3(unsigned(ctas[0] + ctas[1])), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
     return FA_ERR_CUDA;
   if (prm.w[0] && launch_pdl(fa_qk_norm_rope_dw_kernel, dim3(D / 8, 2), dim3(512), 0, st,
-                             static_cast<const float*>(prm.part), dwq, dwk, D, ctas[0], ctas[0] + ctas[1]) != cudaSuccess)
+                             static_cast<const float*>(prm.part), dwq, dwk, D, ctas[0], ctas[0] + ctas[1]) !=
+                                 cudaSuccess)
     return FA_ERR_CUDA;
   return launched();
 }
@@ -186,8 +187,9 @@ fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, const PartParam
 }
 
 fa_status part_check(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                     const int* ctx_lens, const void* o, const float* lse, int R, int Hq, int Hkv, int d, int block_size,
-                     int max_blocks, int num_blocks, float scale, fa_dtype dtype) {
+                     const int* ctx_lens, const void* o, const float* lse, int R, int Hq, int Hkv, int d, int
+                         block_size,
+                     int max_blocks, int num_blocks, float scale, int dtype) {
   if (!q || !k_cache || !v_cache || !block_table || !ctx_lens || !o) return FA_ERR_INVALID_ARG;
   if (!part_sizes(R, Hq, Hkv, d, max_blocks, block_size) || num_blocks <= 0) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
@@ -232,68 +234,64 @@ int evict_cap(int max_blocks, int keep) {
 
 extern "C" {
 
-fa_status fa_qk_norm_rope(const void* q, const void* k, const int64_t* q_strides, const int64_t* k_strides,
-                          const void* q_weight, const void* k_weight, const int* positions, int64_t pos_axis_stride,
-                          int64_t pos_batch_stride, const double* inv_freq, void* q_out, void* k_out, int B, int Hq,
-                          int Hkv, int N, int d, int rotary_dim, const int* sections, int n_axes, int interleaved,
-                          float eps, fa_dtype dtype, void* stream) {
-  const fa_status s = rope_check(positions, inv_freq, B, Hq, Hkv, N, d, rotary_dim, sections, n_axes, interleaved, eps,
-                                 dtype);
+fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* args, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_qk_norm_rope_args& a = *args;
+  const fa_status s = rope_check(a.positions, a.inv_freq, a.B, a.Hq, a.Hkv, a.N, a.d, a.rotary_dim, a.sections,
+                                 a.n_axes, a.interleaved, a.eps,
+                                 a.dtype);
   if (s != FA_OK) return s;
-  if (!rope_rows(q, q_strides, dtype) || !rope_rows(k, k_strides, dtype)) return FA_ERR_INVALID_ARG;
-  if (!q_out || !k_out || !aligned(q_out, 16) || !aligned(k_out, 16)) return FA_ERR_INVALID_ARG;
-  if (!q_weight != !k_weight || !aligned(q_weight, 2) || !aligned(k_weight, 2)) return FA_ERR_INVALID_ARG;
-  RopeParams prm{{q, k, nullptr},
-                 {q_strides[0], k_strides[0], 0},
-                 {q_strides[1], k_strides[1], 0},
-                 {q_strides[2], k_strides[2], 0},
-                 {q_weight, k_weight},
-                 positions, inv_freq,
-                 {q_out, k_out},
-                 pos_axis_stride, pos_batch_stride, B, Hq, Hkv, N, rotary_dim, sections[0],
-                 n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, 1, 1,
+  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype)) return FA_ERR_INVALID_ARG;
+  if (!a.q_out || !a.k_out || !aligned(a.q_out, 16) || !aligned(a.k_out, 16)) return FA_ERR_INVALID_ARG;
+  if (!a.q_weight != !a.k_weight || !aligned(a.q_weight, 2) || !aligned(a.k_weight, 2)) return FA_ERR_INVALID_ARG;
+  RopeParams prm{{a.q, a.k, nullptr},
+                 {a.q_strides[0], a.k_strides[0], 0},
+                 {a.q_strides[1], a.k_strides[1], 0},
+                 {a.q_strides[2], a.k_strides[2], 0},
+                 {a.q_weight, a.k_weight},
+                 a.positions, a.inv_freq,
+                 {a.q_out, a.k_out},
+                 a.pos_axis_stride, a.pos_batch_stride, a.B, a.Hq, a.Hkv, a.N, a.rotary_dim, a.sections[0],
+                 a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1, 1, 1,
                  nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == FA_DTYPE_BF16 ? rope_by_d<__nv_bfloat16>(prm, d, interleaved, st)
-                                : rope_by_d<float>(prm, d, interleaved, st);
+  return a.dtype == FA_DTYPE_BF16 ? rope_by_d<__nv_bfloat16>(prm, a.d, a.interleaved, st)
+                                : rope_by_d<float>(prm, a.d, a.interleaved, st);
 }
 
-fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, const int64_t* q_strides,
-                                 const int64_t* k_strides, const int64_t* v_strides, const void* q_weight,
-                                 const void* k_weight, const int* positions, int64_t pos_axis_stride,
-                                 int64_t pos_batch_stride, const double* inv_freq, void* k_cache, void* v_cache,
-                                 const int* block_table, const int* ctx_lens, const int* q_lens, void* q_out, int R,
-                                 int Hq, int Hkv, int Nq_max, int d, int block_size, int max_blocks_per_seq,
-                                 int num_blocks, int rotary_dim, const int* sections, int n_axes, int interleaved,
-                                 float eps, fa_dtype dtype, void* stream) {
-  const fa_status s = rope_check(positions, inv_freq, R, Hq, Hkv, Nq_max, d, rotary_dim, sections, n_axes, interleaved,
-                                 eps, dtype);
+fa_status fa_qk_norm_rope_append(const fa_qk_norm_rope_append_args* args, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_qk_norm_rope_append_args& a = *args;
+  const fa_status s = rope_check(a.positions, a.inv_freq, a.R, a.Hq, a.Hkv, a.Nq_max, a.d, a.rotary_dim, a.sections,
+                                 a.n_axes, a.interleaved,
+                                 a.eps, a.dtype);
   if (s != FA_OK) return s;
-  if (block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0) return FA_ERR_INVALID_ARG;
-  if (dtype != FA_DTYPE_BF16 || d == 256 || block_size != 16) return FA_ERR_UNSUPPORTED;
-  if (int64_t(max_blocks_per_seq) * 16 > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  if (!rope_rows(q, q_strides, dtype) || !rope_rows(k, k_strides, dtype) || !rope_rows(v, v_strides, dtype))
+  if (a.block_size <= 0 || a.max_blocks_per_seq <= 0 || a.num_blocks <= 0) return FA_ERR_INVALID_ARG;
+  if (a.dtype != FA_DTYPE_BF16 || a.d == 256 || a.block_size != 16) return FA_ERR_UNSUPPORTED;
+  if (int64_t(a.max_blocks_per_seq) * 16 > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) || !rope_rows(a.v, a.v_strides,
+      a.dtype))
     return FA_ERR_INVALID_ARG;
-  if (!q_out || !k_cache || !v_cache || !block_table || !ctx_lens || !q_lens) return FA_ERR_INVALID_ARG;
-  if (!aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
-      !aligned(ctx_lens, 4) || !aligned(q_lens, 4))
+  if (!a.q_out || !a.k_cache || !a.v_cache || !a.block_table || !a.ctx_lens || !a.q_lens) return FA_ERR_INVALID_ARG;
+  if (!aligned(a.q_out, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.block_table, 4) ||
+      !aligned(a.ctx_lens, 4) || !aligned(a.q_lens, 4))
     return FA_ERR_INVALID_ARG;
-  if (!q_weight != !k_weight || !aligned(q_weight, 2) || !aligned(k_weight, 2)) return FA_ERR_INVALID_ARG;
-  RopeParams prm{{q, k, v},
-                 {q_strides[0], k_strides[0], v_strides[0]},
-                 {q_strides[1], k_strides[1], v_strides[1]},
-                 {q_strides[2], k_strides[2], v_strides[2]},
-                 {q_weight, k_weight},
-                 positions, inv_freq,
-                 {q_out, nullptr},
-                 pos_axis_stride, pos_batch_stride, R, Hq, Hkv, Nq_max, rotary_dim, sections[0],
-                 n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, 1, 1,
-                 block_table, ctx_lens, q_lens, k_cache, v_cache, max_blocks_per_seq, num_blocks};
+  if (!a.q_weight != !a.k_weight || !aligned(a.q_weight, 2) || !aligned(a.k_weight, 2)) return FA_ERR_INVALID_ARG;
+  RopeParams prm{{a.q, a.k, a.v},
+                 {a.q_strides[0], a.k_strides[0], a.v_strides[0]},
+                 {a.q_strides[1], a.k_strides[1], a.v_strides[1]},
+                 {a.q_strides[2], a.k_strides[2], a.v_strides[2]},
+                 {a.q_weight, a.k_weight},
+                 a.positions, a.inv_freq,
+                 {a.q_out, nullptr},
+                 a.pos_axis_stride, a.pos_batch_stride, a.R, a.Hq, a.Hkv, a.Nq_max, a.rotary_dim, a.sections[0],
+                 a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1, 1, 1,
+                 a.block_table, a.ctx_lens, a.q_lens, a.k_cache, a.v_cache, a.max_blocks_per_seq, a.num_blocks};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  switch (d) {
-    case 64: return rope_launch<__nv_bfloat16, 64, true>(prm, interleaved, st);
-    case 96: return rope_launch<__nv_bfloat16, 96, true>(prm, interleaved, st);
-    default: return rope_launch<__nv_bfloat16, 128, true>(prm, interleaved, st);
+  switch (a.d) {
+    case 64: return rope_launch<__nv_bfloat16, 64, true>(prm, a.interleaved, st);
+    case 96: return rope_launch<__nv_bfloat16, 96, true>(prm, a.interleaved, st);
+    default: return rope_launch<__nv_bfloat16, 128, true>(prm, a.interleaved, st);
   }
 }
 
@@ -301,57 +299,59 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
   return d <= 0 ? 0 : align256(size_t(kRopeBwdCtas) * d * sizeof(float));
 }
 
-fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, fa_dtype dout_dtype, const void* q, const void* k,
-                              const int64_t* q_strides, const int64_t* k_strides, const void* q_weight,
-                              const void* k_weight, const int* positions, int64_t pos_axis_stride,
-                              int64_t pos_batch_stride, const double* inv_freq, void* dq, void* dk,
-                              const int64_t* dq_strides, const int64_t* dk_strides, fa_dtype grad_dtype, float* dq_weight,
-                              float* dk_weight, int B, int Hq, int Hkv, int N, int d, int rotary_dim,
-                              const int* sections, int n_axes, int interleaved, float eps, fa_dtype dtype,
-                              void* workspace, size_t workspace_bytes, void* stream) {
-  const fa_status s = rope_check(positions, inv_freq, B, Hq, Hkv, N, d, rotary_dim, sections, n_axes, interleaved, eps,
-                                 dtype);
+fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_qk_norm_rope_bwd_args& a = *args;
+  const fa_status s = rope_check(a.positions, a.inv_freq, a.B, a.Hq, a.Hkv, a.N, a.d, a.rotary_dim, a.sections,
+                                 a.n_axes, a.interleaved, a.eps,
+                                 a.dtype);
   if (s != FA_OK) return s;
-  if (!dq_out || !dk_out || !aligned(dq_out, 16) || !aligned(dk_out, 16)) return FA_ERR_INVALID_ARG;
-  if (!q_weight != !k_weight || !aligned(q_weight, 2) || !aligned(k_weight, 2)) return FA_ERR_INVALID_ARG;
-  if (dout_dtype != FA_DTYPE_F32 && dout_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
-  if (grad_dtype != FA_DTYPE_F32 && grad_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
-  if (dtype == FA_DTYPE_F32 && (dout_dtype != FA_DTYPE_F32 || grad_dtype != FA_DTYPE_F32)) return FA_ERR_UNSUPPORTED;
-  if (!rope_rows(q, q_strides, dtype) || !rope_rows(k, k_strides, dtype) || !rope_rows(dq, dq_strides, grad_dtype) ||
-      !rope_rows(dk, dk_strides, grad_dtype))
+  if (!a.dq_out || !a.dk_out || !aligned(a.dq_out, 16) || !aligned(a.dk_out, 16)) return FA_ERR_INVALID_ARG;
+  if (!a.q_weight != !a.k_weight || !aligned(a.q_weight, 2) || !aligned(a.k_weight, 2)) return FA_ERR_INVALID_ARG;
+  if (a.dout_dtype != FA_DTYPE_F32 && a.dout_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
+  if (a.grad_dtype != FA_DTYPE_F32 && a.grad_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
+  if (a.dtype == FA_DTYPE_F32 && (a.dout_dtype != FA_DTYPE_F32 || a.grad_dtype != FA_DTYPE_F32)) return
+      FA_ERR_UNSUPPORTED;
+  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) || !rope_rows(a.dq, a.dq_strides,
+      a.grad_dtype) ||
+      !rope_rows(a.dk, a.dk_strides, a.grad_dtype))
     return FA_ERR_INVALID_ARG;
   // no two rows of a gradient may share memory
-  const int n[2][3] = {{B, Hq, N}, {B, Hkv, N}};
+  const int n[2][3] = {{a.B, a.Hq, a.N}, {a.B, a.Hkv, a.N}};
   for (int t = 0; t < 2; ++t)
     for (int i = 0; i < 3; ++i)
-      if (n[t][i] > 1 && (t ? dk_strides : dq_strides)[i] < d) return FA_ERR_INVALID_ARG;
-  if (q_weight) {
-    if (!dq_weight || !dk_weight || !aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return FA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(d) || !aligned(workspace, 256))
+      if (n[t][i] > 1 && (t ? a.dk_strides : a.dq_strides)[i] < a.d) return FA_ERR_INVALID_ARG;
+  if (a.q_weight) {
+    if (!a.dq_weight || !a.dk_weight || !aligned(a.dq_weight, 4) || !aligned(a.dk_weight, 4)) return FA_ERR_INVALID_ARG;
+    if (!a.workspace || a.workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(a.d) || !aligned(a.workspace, 256))
       return FA_ERR_WORKSPACE;
   }
-  RopeBwdParams prm{{dq_out, dk_out},
-                    {q, k},
-                    {q_strides[0], k_strides[0]},
-                    {q_strides[1], k_strides[1]},
-                    {q_strides[2], k_strides[2]},
-                    {q_weight, k_weight},
-                    positions, inv_freq,
-                    {dq, dk},
-                    {dq_strides[0], dk_strides[0]},
-                    {dq_strides[1], dk_strides[1]},
-                    {dq_strides[2], dk_strides[2]},
-                    static_cast<float*>(workspace),
-                    pos_axis_stride, pos_batch_stride, B, {Hq, Hkv}, N, rotary_dim, sections[0],
-                    n_axes > 1 ? sections[0] + sections[1] : sections[0], eps, 1, {1, 1}, 0};
+  RopeBwdParams prm{{a.dq_out, a.dk_out},
+                    {a.q, a.k},
+                    {a.q_strides[0], a.k_strides[0]},
+                    {a.q_strides[1], a.k_strides[1]},
+                    {a.q_strides[2], a.k_strides[2]},
+                    {a.q_weight, a.k_weight},
+                    a.positions, a.inv_freq,
+                    {a.dq, a.dk},
+                    {a.dq_strides[0], a.dk_strides[0]},
+                    {a.dq_strides[1], a.dk_strides[1]},
+                    {a.dq_strides[2], a.dk_strides[2]},
+                    static_cast<float*>(a.workspace),
+                    a.pos_axis_stride, a.pos_batch_stride, a.B, {a.Hq, a.Hkv}, a.N, a.rotary_dim, a.sections[0],
+                    a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1, {1, 1}, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == FA_DTYPE_F32) return rope_bwd_by_d<float, float, float>(prm, d, interleaved, dq_weight, dk_weight, st);
+  if (a.dtype == FA_DTYPE_F32) return rope_bwd_by_d<float, float, float>(prm, a.d, a.interleaved, a.dq_weight,
+      a.dk_weight, st);
   using bf = __nv_bfloat16;
-  if (dout_dtype == FA_DTYPE_F32)
-    return grad_dtype == FA_DTYPE_F32 ? rope_bwd_by_d<bf, float, float>(prm, d, interleaved, dq_weight, dk_weight, st)
-                                      : rope_bwd_by_d<bf, float, bf>(prm, d, interleaved, dq_weight, dk_weight, st);
-  return grad_dtype == FA_DTYPE_F32 ? rope_bwd_by_d<bf, bf, float>(prm, d, interleaved, dq_weight, dk_weight, st)
-                                    : rope_bwd_by_d<bf, bf, bf>(prm, d, interleaved, dq_weight, dk_weight, st);
+  if (a.dout_dtype == FA_DTYPE_F32)
+    return a.grad_dtype == FA_DTYPE_F32 ? rope_bwd_by_d<bf, float, float>(prm, a.d, a.interleaved, a.dq_weight,
+        a.dk_weight, st)
+                                      : rope_bwd_by_d<bf, float, bf>(prm, a.d, a.interleaved, a.dq_weight, a.dk_weight,
+                                          st);
+  return a.grad_dtype == FA_DTYPE_F32 ? rope_bwd_by_d<bf, bf, float>(prm, a.d, a.interleaved, a.dq_weight, a.dk_weight,
+      st)
+                                    : rope_bwd_by_d<bf, bf, bf>(prm, a.d, a.interleaved, a.dq_weight, a.dk_weight, st);
 }
 
 size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int max_prefix_blocks,
@@ -360,19 +360,21 @@ size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int 
   return part_plan(R, Hq, Hkv, d, max_blocks_per_seq, max_prefix_blocks, false).bytes;
 }
 
-fa_status fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int* prefix_table,
-                                 const int* prefix_len, const int* block_table, const int* ctx_lens, void* o, float* lse,
-                                 int R, int Hq, int Hkv, int d, int block_size, int max_prefix_blocks,
-                                 int max_blocks_per_seq, int num_blocks, float scale, fa_dtype dtype, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
-  if (!prefix_table || !prefix_len || max_prefix_blocks <= 0 || !aligned(prefix_table, 4) || !aligned(prefix_len, 4))
+fa_status fa_paged_decode_shared(const fa_paged_decode_shared_args* args, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_paged_decode_shared_args& a = *args;
+  if (!a.prefix_table || !a.prefix_len || a.max_prefix_blocks <= 0 || !aligned(a.prefix_table, 4) ||
+      !aligned(a.prefix_len, 4))
     return FA_ERR_INVALID_ARG;
-  const fa_status s = part_check(q, k_cache, v_cache, block_table, ctx_lens, o, lse, R, Hq, Hkv, d, block_size,
-                                 max_blocks_per_seq, num_blocks, scale, dtype);
+  const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
+                                 a.d, a.block_size,
+                                 a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
   if (s != FA_OK) return s;
-  if (int64_t(max_prefix_blocks) * part::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  return part_call(q, k_cache, v_cache, prefix_table, prefix_len, block_table, ctx_lens, nullptr, o, lse, R, Hq, Hkv, d,
-                   max_prefix_blocks, max_blocks_per_seq, num_blocks, scale, workspace, workspace_bytes, stream);
+  if (int64_t(a.max_prefix_blocks) * part::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  return part_call(a.q, a.k_cache, a.v_cache, a.prefix_table, a.prefix_len, a.block_table, a.ctx_lens, nullptr, a.o,
+                   a.lse, a.R, a.Hq, a.Hkv, a.d,
+                   a.max_prefix_blocks, a.max_blocks_per_seq, a.num_blocks, a.scale, a.workspace, a.workspace_bytes,
+                       stream);
 }
 
 size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int max_blocks_per_seq, int block_size) {
@@ -380,16 +382,17 @@ size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int 
   return part_plan(R, Hq, Hkv, d, max_blocks_per_seq, 0, true).bytes;
 }
 
-fa_status fa_paged_decode_scored(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                                 const int* ctx_lens, float* weights, void* o, float* lse, int R, int Hq, int Hkv,
-                                 int d, int block_size, int max_blocks_per_seq, int num_blocks, float scale,
-                                 fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!weights || !aligned(weights, 4)) return FA_ERR_INVALID_ARG;
-  const fa_status s = part_check(q, k_cache, v_cache, block_table, ctx_lens, o, lse, R, Hq, Hkv, d, block_size,
-                                 max_blocks_per_seq, num_blocks, scale, dtype);
+fa_status fa_paged_decode_scored(const fa_paged_decode_scored_args* args, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_paged_decode_scored_args& a = *args;
+  if (!a.weights || !aligned(a.weights, 4)) return FA_ERR_INVALID_ARG;
+  const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
+                                 a.d, a.block_size,
+                                 a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
   if (s != FA_OK) return s;
-  return part_call(q, k_cache, v_cache, nullptr, nullptr, block_table, ctx_lens, weights, o, lse, R, Hq, Hkv, d, 0,
-                   max_blocks_per_seq, num_blocks, scale, workspace, workspace_bytes, stream);
+  return part_call(a.q, a.k_cache, a.v_cache, nullptr, nullptr, a.block_table, a.ctx_lens, a.weights, a.o, a.lse, a.R,
+                   a.Hq, a.Hkv, a.d, 0,
+                   a.max_blocks_per_seq, a.num_blocks, a.scale, a.workspace, a.workspace_bytes, stream);
 }
 
 size_t fa_paged_evict_workspace_size(int R, int Hkv, int max_blocks_per_seq, int keep) {
@@ -398,42 +401,46 @@ size_t fa_paged_evict_workspace_size(int R, int Hkv, int max_blocks_per_seq, int
   return align256(n * sizeof(int)) + align256(n * 2 * evict_cap(max_blocks_per_seq, keep) * sizeof(int));
 }
 
-fa_status fa_paged_evict(void* k_cache, void* v_cache, const int* block_table, const int* ctx_lens, const int* seq_lens,
-                         const float* weights, const int* slot_pos, float* weights_out, int* slot_pos_out, int* new_ctx,
-                         int R, int Hkv, int d, int block_size, int max_blocks_per_seq, int num_blocks, int keep,
-                         int recent, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!k_cache || !v_cache || !block_table || !ctx_lens || !seq_lens || !weights || !slot_pos || !weights_out ||
-      !slot_pos_out || !new_ctx)
+fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_paged_evict_args& a = *args;
+  if (!a.k_cache || !a.v_cache || !a.block_table || !a.ctx_lens || !a.seq_lens || !a.weights || !a.slot_pos ||
+      !a.weights_out ||
+      !a.slot_pos_out || !a.new_ctx)
     return FA_ERR_INVALID_ARG;
-  if (R <= 0 || Hkv <= 0 || d <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+  if (a.R <= 0 || a.Hkv <= 0 || a.d <= 0 || a.block_size <= 0 || a.max_blocks_per_seq <= 0 || a.num_blocks <= 0)
     return FA_ERR_INVALID_ARG;
-  if (keep <= 0 || recent < 0 || recent > keep) return FA_ERR_INVALID_ARG;
-  const void* small[] = {block_table, ctx_lens, seq_lens, weights, slot_pos, weights_out, slot_pos_out, new_ctx};
+  if (a.keep <= 0 || a.recent < 0 || a.recent > a.keep) return FA_ERR_INVALID_ARG;
+  const void* small[] = {a.block_table, a.ctx_lens, a.seq_lens, a.weights, a.slot_pos, a.weights_out, a.slot_pos_out,
+      a.new_ctx};
   for (const void* p : small)
     if (!aligned(p, 4)) return FA_ERR_INVALID_ARG;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return FA_ERR_INVALID_ARG;
+  if (!aligned(a.k_cache, 16) || !aligned(a.v_cache, 16)) return FA_ERR_INVALID_ARG;
   // the selection reads its inputs while it writes its outputs
-  if (weights_out == weights || slot_pos_out == slot_pos || new_ctx == ctx_lens || new_ctx == seq_lens)
+  if (a.weights_out == a.weights || a.slot_pos_out == a.slot_pos || a.new_ctx == a.ctx_lens || a.new_ctx == a.seq_lens)
     return FA_ERR_INVALID_ARG;
-  if (dtype != FA_DTYPE_BF16 || (d != 64 && d != 96 && d != 128 && d != 256) || block_size != evict::BS)
+  if (a.dtype != FA_DTYPE_BF16 || (a.d != 64 && a.d != 96 && a.d != 128 && a.d != 256) || a.block_size != evict::BS)
     return FA_ERR_UNSUPPORTED;
-  if (R > 65535 || Hkv > 65535 || int64_t(max_blocks_per_seq) * evict::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < fa_paged_evict_workspace_size(R, Hkv, max_blocks_per_seq, keep) ||
-      !aligned(workspace, 256))
+  if (a.R > 65535 || a.Hkv > 65535 || int64_t(a.max_blocks_per_seq) * evict::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  if (!a.workspace || a.workspace_bytes < fa_paged_evict_workspace_size(a.R, a.Hkv, a.max_blocks_per_seq, a.keep) ||
+      !aligned(a.workspace, 256))
     return FA_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
-  EvictParams prm{block_table, ctx_lens, seq_lens, weights, slot_pos, weights_out, slot_pos_out, new_ctx,
-                  reinterpret_cast<int*>(ws + align256(size_t(R) * Hkv * sizeof(int))), reinterpret_cast<int*>(ws),
-                  static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache), R, Hkv, max_blocks_per_seq, num_blocks,
-                  keep, recent, evict_cap(max_blocks_per_seq, keep), d * 2 / 16};
+  char* ws = static_cast<char*>(a.workspace);
+  EvictParams prm{a.block_table, a.ctx_lens, a.seq_lens, a.weights, a.slot_pos, a.weights_out, a.slot_pos_out,
+      a.new_ctx,
+                  reinterpret_cast<int*>(ws + align256(size_t(a.R) * a.Hkv * sizeof(int))), reinterpret_cast<int*>(ws),
+                  static_cast<uint4*>(a.k_cache), static_cast<uint4*>(a.v_cache), a.R, a.Hkv, a.max_blocks_per_seq,
+                      a.num_blocks,
+                  a.keep, a.recent, evict_cap(a.max_blocks_per_seq, a.keep), a.d * 2 / 16};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_pdl(fa_evict_select_kernel, dim3(Hkv, R), dim3(evict::THREADS), 0, st, prm) != cudaSuccess)
+  if (launch_pdl(fa_evict_select_kernel, dim3(a.Hkv, a.R), dim3(evict::THREADS), 0, st, prm) != cudaSuccess)
     return FA_ERR_CUDA;
   if (prm.cap > 0) {
     const int64_t pieces = int64_t(prm.cap) * 2 * prm.row16;
-    const int64_t want = std::max<int64_t>(1, 148 * 8 / (int64_t(R) * Hkv));
+    const int64_t want = std::max<int64_t>(1, 148 * 8 / (int64_t(a.R) * a.Hkv));
     const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(want, (pieces + 255) / 256)));
-    if (launch_pdl(fa_evict_move_kernel, dim3(grid, Hkv, R), dim3(256), 0, st, prm) != cudaSuccess) return FA_ERR_CUDA;
+    if (launch_pdl(fa_evict_move_kernel, dim3(grid, a.Hkv, a.R), dim3(256), 0, st, prm) != cudaSuccess) return
+        FA_ERR_CUDA;
   }
   return launched();
 }

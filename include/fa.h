@@ -239,6 +239,11 @@ fa_status fa_paged_decode_noalloc(const void* q, const void* k_cache, const void
                                   int num_blocks, float scale, fa_dtype dtype, void* stream);
 
 /*
+ * The passes around attention below take their arguments in one struct (read on the host during
+ * the call): the fields that the comments name, pointers as everywhere, dtypes as fa_dtype.
+ */
+
+/*
  * Norm and rotation of q and k — the pass before attention (no counterpart on the pages).
  * Per head row x [d] with weight w [d] and n_axes positions per token:
  *   r = (mean_c x_c^2 + eps)^(-1/2),  y = x r w;  without weights y = x,
@@ -247,12 +252,12 @@ fa_status fa_paged_decode_noalloc(const void* q, const void* k_cache, const void
  * Pair i of the rotary_dim / 2 pairs is (i, i + rotary_dim / 2), or (2i, 2i + 1) where
  * interleaved is 1; values at and past rotary_dim do not turn.  The first sections[0] pairs
  * follow axis 0 (time), the next sections[1] axis 1 (height), the last sections[2] axis 2
- * (width); the n_axes sections (1 to 3, host array) sum to rotary_dim / 2.  Any int32 position
+ * (width); the n_axes sections (1 to 3) sum to rotary_dim / 2.  Any int32 position
  * is exact: the angle is reduced in 64 bits.  Products, sums and the norm are fp32, rounded
  * once at the end.
  *
  * Common arguments:
- *   q_strides, k_strides (, v_strides): host arrays {batch, head, token} in elements, multiples
+ *   q_strides, k_strides (, v_strides): {batch, head, token} in elements, multiples
  *     of 16 bytes, so that views of a fused projection [B, N, heads, d] are read in place; a
  *     head's d values are contiguous.  0 repeats a row.
  *   q_weight, k_weight [d] of dtype `dtype`, or both NULL: no norm, the rotation alone.
@@ -269,11 +274,17 @@ fa_status fa_paged_decode_noalloc(const void* q, const void* k_cache, const void
  * Errors: FA_ERR_INVALID_ARG (null or misaligned pointer, bad size, stride, section, flag or
  * eps, one weight without the other); FA_ERR_UNSUPPORTED (other d, rotary_dim or dtype).
  */
-fa_status fa_qk_norm_rope(const void* q, const void* k, const int64_t* q_strides, const int64_t* k_strides,
-                          const void* q_weight, const void* k_weight, const int* positions, int64_t pos_axis_stride,
-                          int64_t pos_batch_stride, const double* inv_freq, void* q_out, void* k_out, int B, int Hq,
-                          int Hkv, int N, int d, int rotary_dim, const int* sections, int n_axes, int interleaved,
-                          float eps, fa_dtype dtype, void* stream);
+typedef struct {
+  const void *q, *k, *q_weight, *k_weight;
+  const int* positions;
+  const double* inv_freq;
+  void *q_out, *k_out;
+  int64_t q_strides[3], k_strides[3], pos_axis_stride, pos_batch_stride;
+  int B, Hq, Hkv, N, d, rotary_dim, sections[3], n_axes, interleaved;
+  float eps;
+  int dtype;
+} fa_qk_norm_rope_args;
+fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* args, void* stream);
 
 /*
  * fa_qk_norm_rope_append — the serving form: the same on R requests, with k' and v written
@@ -291,14 +302,19 @@ fa_status fa_qk_norm_rope(const void* q, const void* k, const int64_t* q_strides
  *   write; either sets the device status word (FA_ERR_INVALID_ARG).  No two tokens of a call may
  *   share a cache slot.
  */
-fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, const int64_t* q_strides,
-                                 const int64_t* k_strides, const int64_t* v_strides, const void* q_weight,
-                                 const void* k_weight, const int* positions, int64_t pos_axis_stride,
-                                 int64_t pos_batch_stride, const double* inv_freq, void* k_cache, void* v_cache,
-                                 const int* block_table, const int* ctx_lens, const int* q_lens, void* q_out, int R,
-                                 int Hq, int Hkv, int Nq_max, int d, int block_size, int max_blocks_per_seq,
-                                 int num_blocks, int rotary_dim, const int* sections, int n_axes, int interleaved,
-                                 float eps, fa_dtype dtype, void* stream);
+typedef struct {
+  const void *q, *k, *v, *q_weight, *k_weight;
+  const int* positions;
+  const double* inv_freq;
+  void *k_cache, *v_cache;
+  const int *block_table, *ctx_lens, *q_lens;
+  void* q_out;
+  int64_t q_strides[3], k_strides[3], v_strides[3], pos_axis_stride, pos_batch_stride;
+  int R, Hq, Hkv, Nq_max, d, block_size, max_blocks_per_seq, num_blocks, rotary_dim, sections[3], n_axes, interleaved;
+  float eps;
+  int dtype;
+} fa_qk_norm_rope_append_args;
+fa_status fa_qk_norm_rope_append(const fa_qk_norm_rope_append_args* args, void* stream);
 
 /* fa_qk_norm_rope_bwd_workspace_size — bytes of device workspace fa_qk_norm_rope_bwd needs for its
  * partial weight gradients (none without weights).  Returns 0 for an invalid d. */
@@ -307,7 +323,7 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
 /*
  * fa_qk_norm_rope_bwd — gradients of fa_qk_norm_rope, recomputing the norm from q and k.
  *   dq_out [B,Hq,N,d], dk_out [B,Hkv,N,d] contiguous, of dtype dout_dtype (what fa_bwd writes).
- *   q, k by strides, of dtype `dtype` (without weights only their type matters; they may be NULL).
+ *   q, k by strides, of dtype `dtype` (not read without weights).
  *   dq, dk of dtype grad_dtype by dq_strides, dk_strides (the projection's layout, for example);
  *   strides of dimensions larger than 1 must be at least d, and no two rows may share memory.
  *   dq_weight, dk_weight [d] fp32: the sums over every row of q, of k (with weights only).  The
@@ -316,14 +332,20 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  *   workspace: at least fa_qk_norm_rope_bwd_workspace_size(d) bytes, 256-byte aligned.
  * Errors: as fa_qk_norm_rope, plus FA_ERR_WORKSPACE.
  */
-fa_status fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, fa_dtype dout_dtype, const void* q, const void* k,
-                              const int64_t* q_strides, const int64_t* k_strides, const void* q_weight,
-                              const void* k_weight, const int* positions, int64_t pos_axis_stride,
-                              int64_t pos_batch_stride, const double* inv_freq, void* dq, void* dk,
-                              const int64_t* dq_strides, const int64_t* dk_strides, fa_dtype grad_dtype, float* dq_weight,
-                              float* dk_weight, int B, int Hq, int Hkv, int N, int d, int rotary_dim,
-                              const int* sections, int n_axes, int interleaved, float eps, fa_dtype dtype,
-                              void* workspace, size_t workspace_bytes, void* stream);
+typedef struct {
+  const void *dq_out, *dk_out, *q, *k, *q_weight, *k_weight;
+  const int* positions;
+  const double* inv_freq;
+  void *dq, *dk;
+  float *dq_weight, *dk_weight;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t q_strides[3], k_strides[3], dq_strides[3], dk_strides[3], pos_axis_stride, pos_batch_stride;
+  int B, Hq, Hkv, N, d, rotary_dim, sections[3], n_axes, interleaved;
+  float eps;
+  int dtype, dout_dtype, grad_dtype;
+} fa_qk_norm_rope_bwd_args;
+fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream);
 
 /* fa_paged_decode_shared_workspace_size — bytes of device workspace fa_paged_decode_shared needs
  * for its partial results.  Returns 0 for invalid sizes. */
@@ -344,11 +366,18 @@ size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int 
  *   (FA_ERR_INVALID_ARG); the results it belongs to are undefined.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.
  */
-fa_status fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, const int* prefix_table,
-                                 const int* prefix_len, const int* block_table, const int* ctx_lens, void* o, float* lse,
-                                 int R, int Hq, int Hkv, int d, int block_size, int max_prefix_blocks,
-                                 int max_blocks_per_seq, int num_blocks, float scale, fa_dtype dtype, void* workspace,
-                                 size_t workspace_bytes, void* stream);
+typedef struct {
+  const void *q, *k_cache, *v_cache;
+  const int *prefix_table, *prefix_len, *block_table, *ctx_lens;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int R, Hq, Hkv, d, block_size, max_prefix_blocks, max_blocks_per_seq, num_blocks;
+  float scale;
+  int dtype;
+} fa_paged_decode_shared_args;
+fa_status fa_paged_decode_shared(const fa_paged_decode_shared_args* args, void* stream);
 
 /* fa_paged_decode_scored_workspace_size — bytes of device workspace fa_paged_decode_scored needs
  * for its partial results and scores.  Returns 0 for invalid sizes. */
@@ -364,10 +393,19 @@ size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int 
  *   d in {64, 128}, block_size == 16, Hq / Hkv <= 16, dtype BF16.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.
  */
-fa_status fa_paged_decode_scored(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                                 const int* ctx_lens, float* weights, void* o, float* lse, int R, int Hq, int Hkv,
-                                 int d, int block_size, int max_blocks_per_seq, int num_blocks, float scale,
-                                 fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+typedef struct {
+  const void *q, *k_cache, *v_cache;
+  const int *block_table, *ctx_lens;
+  float* weights;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int R, Hq, Hkv, d, block_size, max_blocks_per_seq, num_blocks;
+  float scale;
+  int dtype;
+} fa_paged_decode_scored_args;
+fa_status fa_paged_decode_scored(const fa_paged_decode_scored_args* args, void* stream);
 
 /* fa_paged_evict_workspace_size — bytes of device workspace fa_paged_evict needs for its lists of
  * moves.  Returns 0 for invalid sizes. */
@@ -396,10 +434,18 @@ size_t fa_paged_evict_workspace_size(int R, int Hkv, int max_blocks_per_seq, int
  *   either sets the device status word (FA_ERR_INVALID_ARG).
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.
  */
-fa_status fa_paged_evict(void* k_cache, void* v_cache, const int* block_table, const int* ctx_lens, const int* seq_lens,
-                         const float* weights, const int* slot_pos, float* weights_out, int* slot_pos_out, int* new_ctx,
-                         int R, int Hkv, int d, int block_size, int max_blocks_per_seq, int num_blocks, int keep,
-                         int recent, fa_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+typedef struct {
+  void *k_cache, *v_cache;
+  const int *block_table, *ctx_lens, *seq_lens;
+  const float* weights;
+  const int* slot_pos;
+  float* weights_out;
+  int *slot_pos_out, *new_ctx;
+  void* workspace;
+  size_t workspace_bytes;
+  int R, Hkv, d, block_size, max_blocks_per_seq, num_blocks, keep, recent, dtype;
+} fa_paged_evict_args;
+fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream);
 
 /*
  * fa_device_status — synchronises the current device and returns the device status

@@ -1,6 +1,4 @@
 """The entry points of the passes around attention refuse bad arguments on the host.  Runs without a GPU."""
-import ctypes
-
 import pytest
 import torch
 
@@ -8,8 +6,6 @@ import exact_attention_128_b200 as fa
 from exact_attention_128_b200 import build as fabuild
 
 FAKE = 1 << 20  # 16-byte aligned, never dereferenced: every call below is rejected on the host
-I64 = ctypes.c_int64 * 3
-I3 = ctypes.c_int * 3
 BAD, UNS, WS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_ERR_WORKSPACE
 
 
@@ -19,61 +15,64 @@ def L():
     return fa.lib()
 
 
-def call(fn, base, kw):
+def call(L, name, base, kw):
+    """Pack base, with the changes kw, as the entry point's struct."""
     assert set(kw) <= set(base), kw
-    return fn(*{**base, **kw}.values())
+    flat = []
+    for v in {**base, **kw}.values():
+        flat += v if isinstance(v, (list, tuple)) else [0 if v is None else v]
+    return getattr(L, name)(fa.PACKED[name](*flat), None)
 
 
-ST = dict(q_strides=I64(2048, 64, 512), k_strides=I64(2048, 64, 512))
-ROPE_TAIL = dict(rotary_dim=64, sections=I3(32, 0, 0), n_axes=1, interleaved=0, eps=1e-6, dtype=fa.FA_DTYPE_BF16)
-FWD = dict(q=FAKE, k=FAKE, **ST, wq=FAKE, wk=FAKE, pos=FAKE, pos_sa=0, pos_sb=0, freq=FAKE, qo=FAKE, ko=FAKE, B=1, Hq=4,
-           Hkv=2, N=4, d=64, **ROPE_TAIL, stream=None)
-APPEND = dict(q=FAKE, k=FAKE, v=FAKE, **ST, v_strides=I64(2048, 64, 512), wq=FAKE, wk=FAKE, pos=FAKE, pos_sa=0, pos_sb=0,
-              freq=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, ctx=FAKE, ql=FAKE, qo=FAKE, R=1, Hq=4, Hkv=2, N=4, d=64, bs=16,
-              maxb=4, nblocks=10, **ROPE_TAIL, stream=None)
-BWD = dict(dqo=FAKE, dko=FAKE, gin=fa.FA_DTYPE_F32, q=FAKE, k=FAKE, **ST, wq=FAKE, wk=FAKE, pos=FAKE, pos_sa=0, pos_sb=0,
-           freq=FAKE, dq=FAKE, dk=FAKE, dq_strides=I64(2048, 64, 512), dk_strides=I64(2048, 64, 512),
-           gout=fa.FA_DTYPE_BF16, dwq=FAKE, dwk=FAKE, B=2, Hq=4, Hkv=2, N=4, d=64, **ROPE_TAIL, ws=FAKE, ws_bytes=1 << 30,
-           stream=None)
-SHARED = dict(q=FAKE, kc=FAKE, vc=FAKE, pt=FAKE, pl=FAKE, bt=FAKE, ctx=FAKE, o=FAKE, lse=None, R=4, Hq=12, Hkv=2, d=128,
-              bs=16, pb=8, maxb=4, nblocks=100, scale=0.088, dtype=fa.FA_DTYPE_BF16, ws=FAKE, ws_bytes=1 << 40, stream=None)
-SCORED = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, ctx=FAKE, w=FAKE, o=FAKE, lse=None, R=4, Hq=12, Hkv=2, d=128, bs=16,
-              maxb=4, nblocks=100, scale=0.088, dtype=fa.FA_DTYPE_BF16, ws=FAKE, ws_bytes=1 << 40, stream=None)
-EVICT = dict(kc=FAKE, vc=FAKE, bt=FAKE, ctx=FAKE, seq=FAKE, w=FAKE, sp=FAKE, wo=2 * FAKE, so=2 * FAKE, nc=2 * FAKE, R=4,
-             Hkv=2, d=128, bs=16, maxb=4, nblocks=100, keep=8, recent=4, dtype=fa.FA_DTYPE_BF16, ws=FAKE,
-             ws_bytes=1 << 40, stream=None)
+SX, ROW = (32, 0, 0), (2048, 64, 512)  # sections; strides of [1, 4, 4, 64] in a projection
+X = dict(q=FAKE, k=FAKE)
+W = dict(wq=FAKE, wk=FAKE, pos=FAKE, freq=FAKE)
+TAIL = dict(rotary_dim=64, sections=SX, n_axes=1, interleaved=0, eps=1e-6, dtype=fa.FA_DTYPE_BF16)
+FWD = dict(**X, **W, qo=FAKE, ko=FAKE, q_strides=ROW, k_strides=ROW, pos_sa=0, pos_sb=0, B=1, Hq=4, Hkv=2, N=4, d=64, **TAIL)
+APPEND = dict(**X, v=FAKE, **W, kc=FAKE, vc=FAKE, bt=FAKE, ctx=FAKE, ql=FAKE, qo=FAKE, q_strides=ROW, k_strides=ROW,
+              v_strides=ROW, pos_sa=0, pos_sb=0, R=1, Hq=4, Hkv=2, N=4, d=64, bs=16, maxb=4, nblocks=10, **TAIL)
+BWD = dict(dqo=FAKE, dko=FAKE, **X, **W, dq=FAKE, dk=FAKE, dwq=FAKE, dwk=FAKE, ws=FAKE, ws_bytes=1 << 30, q_strides=ROW,
+           k_strides=ROW, dq_strides=ROW, dk_strides=ROW, pos_sa=0, pos_sb=0, B=2, Hq=4, Hkv=2, N=4, d=64, **TAIL,
+           gin=fa.FA_DTYPE_F32, gout=fa.FA_DTYPE_BF16)
+SPACE = dict(ws=FAKE, ws_bytes=1 << 40)
+SHARED = dict(q=FAKE, kc=FAKE, vc=FAKE, pt=FAKE, pl=FAKE, bt=FAKE, ctx=FAKE, o=FAKE, lse=None, **SPACE, R=4, Hq=12, Hkv=2,
+              d=128, bs=16, pb=8, maxb=4, nblocks=100, scale=0.088, dtype=fa.FA_DTYPE_BF16)
+SCORED = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, ctx=FAKE, w=FAKE, o=FAKE, lse=None, **SPACE, R=4, Hq=12, Hkv=2, d=128,
+              bs=16, maxb=4, nblocks=100, scale=0.088, dtype=fa.FA_DTYPE_BF16)
+EVICT = dict(kc=FAKE, vc=FAKE, bt=FAKE, ctx=FAKE, seq=FAKE, w=FAKE, sp=FAKE, wo=2 * FAKE, so=2 * FAKE, nc=2 * FAKE, **SPACE,
+             R=4, Hkv=2, d=128, bs=16, maxb=4, nblocks=100, keep=8, recent=4, dtype=fa.FA_DTYPE_BF16)
 
 ROTARY = [
-    (dict(pos=None), BAD), (dict(freq=None), BAD), (dict(freq=FAKE + 4), BAD), (dict(sections=None), BAD),
-    (dict(sections=I3(31, 0, 0)), BAD), (dict(n_axes=0), BAD), (dict(n_axes=4), BAD), (dict(n_axes=2, sections=I3(33, -1, 0)), BAD),
+    (dict(pos=None), BAD), (dict(freq=None), BAD), (dict(freq=FAKE + 4), BAD),
+    (dict(sections=(31, 0, 0)), BAD), (dict(n_axes=0), BAD), (dict(n_axes=4), BAD), (dict(n_axes=2, sections=(33, -1, 0)), BAD),
     (dict(eps=0.0), BAD), (dict(eps=float("nan")), BAD), (dict(interleaved=2), BAD), (dict(rotary_dim=128), BAD),
-    (dict(rotary_dim=0), BAD), (dict(wq=None), BAD), (dict(q_strides=I64(2048, 68, 512)), BAD), (dict(q_strides=None), BAD),
+    (dict(rotary_dim=0), BAD), (dict(wq=None), BAD), (dict(q_strides=(2048, 68, 512)), BAD),
     (dict(k=FAKE + 2), BAD), (dict(Hq=0), BAD), (dict(d=80), UNS), (dict(dtype=3), UNS),
-    (dict(rotary_dim=24, sections=I3(12, 0, 0)), UNS),
+    (dict(rotary_dim=24, sections=(12, 0, 0)), UNS),
 ]
 
 
 @pytest.mark.parametrize("kw,code", ROTARY + [(dict(q=None), BAD), (dict(qo=None), BAD), (dict(ko=FAKE + 4), BAD)])
 def test_rope_rejects_on_host(L, kw, code):
-    assert call(L.fa_qk_norm_rope, FWD, kw) == code
+    assert call(L, "fa_qk_norm_rope", FWD, kw) == code
 
 
 @pytest.mark.parametrize(
     "kw,code",
-    ROTARY + [(dict(v=None), BAD), (dict(v_strides=I64(2048, 4, 512)), BAD), (dict(bt=None), BAD), (dict(ql=FAKE + 1), BAD),
+    ROTARY + [(dict(v=None), BAD), (dict(v_strides=(2048, 4, 512)), BAD), (dict(bt=None), BAD), (dict(ql=FAKE + 1), BAD),
               (dict(qo=None), BAD), (dict(maxb=0), BAD), (dict(nblocks=-1), BAD), (dict(bs=32), UNS), (dict(d=256), UNS),
               (dict(dtype=fa.FA_DTYPE_F32), UNS)])
 def test_append_rejects_on_host(L, kw, code):
-    assert call(L.fa_qk_norm_rope_append, APPEND, kw) == code
+    assert call(L, "fa_qk_norm_rope_append", APPEND, kw) == code
 
 
 @pytest.mark.parametrize(
     "kw,code",
-    ROTARY + [(dict(dqo=None), BAD), (dict(dk=None), BAD), (dict(dwq=None), BAD), (dict(dq_strides=I64(0, 64, 512)), BAD),
-              (dict(dk_strides=I64(2048, 32, 512)), BAD), (dict(gin=5), UNS), (dict(gout=5), UNS),
+    ROTARY + [(dict(dqo=None), BAD), (dict(dk=None), BAD), (dict(dwq=None), BAD), (dict(dq_strides=(0, 64, 512)), BAD),
+              (dict(dk_strides=(2048, 32, 512)), BAD), (dict(gin=5), UNS), (dict(gout=5), UNS),
               (dict(dtype=fa.FA_DTYPE_F32), UNS), (dict(ws=None), WS), (dict(ws_bytes=16), WS), (dict(ws=FAKE + 16), WS)])
 def test_rope_bwd_rejects_on_host(L, kw, code):
-    assert call(L.fa_qk_norm_rope_bwd, BWD, kw) == code
+    assert call(L, "fa_qk_norm_rope_bwd", BWD, kw) == code
 
 
 DECODE = [
@@ -87,12 +86,12 @@ DECODE = [
 
 @pytest.mark.parametrize("kw,code", DECODE + [(dict(pt=None), BAD), (dict(pl=FAKE + 2), BAD), (dict(pb=0), BAD)])
 def test_shared_rejects_on_host(L, kw, code):
-    assert call(L.fa_paged_decode_shared, SHARED, kw) == code
+    assert call(L, "fa_paged_decode_shared", SHARED, kw) == code
 
 
 @pytest.mark.parametrize("kw,code", DECODE + [(dict(w=None), BAD), (dict(w=FAKE + 2), BAD)])
 def test_scored_rejects_on_host(L, kw, code):
-    assert call(L.fa_paged_decode_scored, SCORED, kw) == code
+    assert call(L, "fa_paged_decode_scored", SCORED, kw) == code
 
 
 @pytest.mark.parametrize(
@@ -102,7 +101,31 @@ def test_scored_rejects_on_host(L, kw, code):
      (dict(so=FAKE), BAD), (dict(nc=FAKE), BAD), (dict(d=80), UNS), (dict(bs=8), UNS), (dict(dtype=fa.FA_DTYPE_F32), UNS),
      (dict(R=70000), UNS), (dict(maxb=1 << 28), UNS), (dict(ws=None), WS), (dict(ws_bytes=16), WS)])
 def test_evict_rejects_on_host(L, kw, code):
-    assert call(L.fa_paged_evict, EVICT, kw) == code
+    assert call(L, "fa_paged_evict", EVICT, kw) == code
+
+
+def test_null_struct_is_refused(L):
+    for name in fa.PACKED:
+        assert getattr(L, name)(None, None) == BAD
+
+
+def test_structs_match_the_header(L, tmp_path):
+    """The binding's packers fill exactly the C structs: their sizes, and one field near each end."""
+    import os
+    import subprocess
+
+    names = list(fa.PACKED)
+    body = "".join(f'printf("%zu %zu\\n", sizeof({n}_args), offsetof({n}_args, dtype));' for n in names)
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include "fa.h"\nint main(void){' + body + "return 0;}")
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["gcc", "-I", inc, "-o", str(tmp_path / "s"), str(src)], check=True)
+    out = subprocess.run([str(tmp_path / "s")], check=True, capture_output=True, text=True).stdout.split()
+    for i, n in enumerate(names):
+        size, at = int(out[2 * i]), int(out[2 * i + 1])
+        packed = fa.PACKED[n].__self__
+        last = 2 if n == "fa_qk_norm_rope_bwd" else 0  # ints behind dtype
+        assert packed.size + (-packed.size) % 8 == size and at == packed.size - 4 * (1 + last), n
 
 
 def test_workspace_sizes(L):
