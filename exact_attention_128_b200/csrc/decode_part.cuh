@@ -20,10 +20,13 @@
 namespace fa {
 namespace part {
 constexpr int WARPS = 4;
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
 constexpr int BS = 16;
 constexpr int ROWS = 16;       // query rows of a piece
 constexpr int MIN_CHUNK = 8;   // blocks of a piece, at least: two for each warp
+constexpr int MAX_PARTS = 64;  // pieces of a row, at most, of either kind
+constexpr int PREFIX_CTAS = 148;  // CTAs of the tensor-core prefix kernel, at most
+constexpr int JOIN_TOKENS = 1024;  // tokens whose weights one CTA adds up
 
 template <int D>
 struct Cfg {
@@ -52,6 +55,10 @@ struct PartParams {
   int parts;               // partial results per row: prefix pieces, then own pieces
   int prefix_parts;
   int chunk, prefix_chunk;  // blocks of a piece
+  // the prefix part by the tensor-core kernel (shared_prefix.cuh): its results, else null
+  const float *pre_o, *pre_lse;
+  int pre_parts, pairs, RT;
+  bool late_wait;  // the grid before this one is that kernel, and nothing of it is read here
   float scale_log2;
   uint64_t wait_ns;
 };
@@ -75,13 +82,20 @@ __global__ void __launch_bounds__(part::WARPS * 32)
   uint8_t* dsmem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~uintptr_t(1023));
   const int s = blockIdx.x, g = blockIdx.y, z = blockIdx.z;  // piece, kv head, request or row tile
   const int G = p.Hq / p.Hkv;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // late_wait: the prefix kernel let this grid start once it had waited for everything before it.
+  // Its own results are read by the grid after this one, which waits for this grid alone: so one
+  // CTA, the last to be started, holds this grid open until the prefix kernel is done.
+  const bool hold = p.late_wait && s == int(gridDim.x) - 1 && g == int(gridDim.y) - 1 && z == int(gridDim.z) - 1;
+  auto finish = [&] {
+    if (hold) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  if (!p.late_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = PREFIX ? part_len(p.plen, 0, p.prefix_blocks, 302) : part_len(p.ctx, z, p.max_blocks, 300);
   const int chunk = PREFIX ? p.prefix_chunk : p.chunk;
   const int nblk = (n + BS - 1) / BS;
   const int b0 = s * chunk;
-  if (n <= 0 || b0 >= nblk) return;
+  if (n <= 0 || b0 >= nblk) return finish();
   const int b1 = min(nblk, b0 + chunk);
   const int* bt = PREFIX ? p.pbt : p.bt + size_t(z) * p.max_blocks;
   const int rows = PREFIX ? min(ROWS, p.R * G - z * ROWS) : G;
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(part::WARPS * 32)
   const int part = PREFIX ? s : p.prefix_parts + s;
   if (abort_flag) {  // NaN, so that nothing merged from this piece looks valid
     for (int i = threadIdx.x; i < rows; i += WARPS * 32) p.part_lse[size_t(row_of(i)) * p.parts + part] = NAN;
-    return;
+    return finish();
   }
   float* so = reinterpret_cast<float*>(dsmem);  // [WARPS][ROWS][OP]
   float* sm = so + WARPS * ROWS * C::OP;        // [WARPS][ROWS]
@@ -312,68 +326,122 @@ __global__ void __launch_bounds__(part::WARPS * 32)
     p.part_o[pi * D + d] = U / L;
     if (d == 0) p.part_lse[pi] = M + __log2f(L);
   }
+  finish();
 }
 
-// Pieces of row (r, h): prefix pieces in [0, np), own pieces in [prefix_parts, prefix_parts + no).
-__device__ __forceinline__ void part_counts(const PartParams& p, int r, int& np, int& no) {
-  const int n = p.ctx[r], P = p.plen ? p.plen[0] : 0;
-  const bool bad = n < 0 || n > p.max_blocks * part::BS || P < 0 || P > p.prefix_blocks * part::BS;
-  np = bad || P == 0 ? 0 : ((P + part::BS - 1) / part::BS + p.prefix_chunk - 1) / p.prefix_chunk;
-  no = bad ? 0 : ((n + part::BS - 1) / part::BS + p.chunk - 1) / p.chunk;
-}
-
-// One CTA per row (r, h), one thread per column: joins the row's pieces.
-template <int D>
-__global__ void __launch_bounds__(D) fa_decode_merge_kernel(const __grid_constant__ PartParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int row = blockIdx.x, d = threadIdx.x;
-  int np, no;
-  part_counts(p, row / p.Hq, np, no);
-  const float* pl = p.part_lse + size_t(row) * p.parts;
-  const float* po = p.part_o + size_t(row) * p.parts * D + d;
-  float M = -INFINITY;
-  bool aborted = false;
-  for (int k = 0; k < np + no; ++k) {
-    const float v = pl[k < np ? k : p.prefix_parts + k - np];
-    M = fmaxf(M, v);
-    aborted |= isnan(v);
+// How the tiles of a prefix of P tokens are dealt out by the tensor-core kernel: CTA c < ctas takes
+// [begin(c), begin(c + 1)) of the items' tiles.
+struct PrefixDeal {
+  static constexpr int BN = 64;
+  int nt, ctas;
+  long long all;
+  __device__ PrefixDeal(int P, int items) {
+    nt = (P + BN - 1) / BN;
+    all = (long long)(items)*nt;
+    // at least two tiles per CTA: a single one does not pay for its partial result
+    ctas = int(min((all + 1) / 2, (long long)(part::PREFIX_CTAS)));
   }
-  float W = 0.f, U = 0.f;
-  for (int k = 0; k < np + no; ++k) {
-    const int s = k < np ? k : p.prefix_parts + k - np;
-    const float w = ex2(pl[s] - M);
-    W += w;
-    U += w * po[size_t(s) * D];
-  }
-  const bool empty = np + no == 0;  // no key at all: o = 0, lse = -inf
-  p.o[size_t(row) * D + d] = __float2bfloat16_rn(aborted ? NAN : empty ? 0.f : U / W);
-  if (d == 0 && p.lse) p.lse[row] = aborted ? NAN : empty ? -INFINITY : (M + __log2f(W)) * 0.69314718055994531f;
-}
+  __device__ long long begin(int c) const { return c * all / ctas; }
+  __device__ int owner(long long x) const { return int(((x + 1) * ctas - 1) / all); }
+};
 
-// weights[r, g, s] += sum over the heads of kv head g of e^{score - lse}, for the cached slots.
-__global__ void __launch_bounds__(256) fa_decode_weights_kernel(const __grid_constant__ PartParams p) {
-  __shared__ float s_lse[part::ROWS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// Joins the pieces of the G rows of (request, kv head).  The last CTA of x writes o and lse; SCORED:
+// the others add up the weights of JOIN_TOKENS tokens each,
+//   weights[r, g, s] += sum over the heads of kv head g of e^{score - lse}.
+template <int D, bool SCORED>
+__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ PartParams p) {
+  using namespace part;
+  __shared__ float s_w[ROWS][MAX_PARTS + PREFIX_CTAS + 1];  // pieces' lse, then their weights
+  __shared__ float s_lse[ROWS];
   const int g = blockIdx.y, r = blockIdx.z, G = p.Hq / p.Hkv;
-  int np, no;
-  part_counts(p, r, np, no);
-  const int n = p.ctx[r];
-  if (no == 0 || int(blockIdx.x) * 256 >= n) return;
-  if (threadIdx.x < G) {
-    const float* pl = p.part_lse + (size_t(r) * p.Hq + g * G + threadIdx.x) * p.parts;
+  const bool join = blockIdx.x == gridDim.x - 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = p.ctx[r], P = p.plen ? p.plen[0] : 0;
+  const bool bad = n < 0 || n > p.max_blocks * BS || P < 0 || P > p.prefix_blocks * BS;
+  if (SCORED && !join && (bad || int(blockIdx.x) * JOIN_TOKENS >= n)) return;
+  const int no = bad ? 0 : ((n + BS - 1) / BS + p.chunk - 1) / p.chunk;
+  int np = 0;
+  size_t pre0 = 0;  // first row of the prefix kernel's results for these rows, and their distance
+  constexpr size_t PRE_STEP = 256;
+  if (!bad && P > 0) {
+    if (p.pre_o) {
+      const int tile = r / p.RT, it = g * p.pairs + tile / 2;
+      const PrefixDeal deal(P, p.Hkv * p.pairs);
+      np = deal.owner((long long)(it + 1) * deal.nt - 1) - deal.owner((long long)(it)*deal.nt) + 1;
+      pre0 = (size_t(it) * p.pre_parts * 2 + (tile & 1)) * 128 + (r - tile * p.RT) * G;
+    } else {
+      np = ((P + BS - 1) / BS + p.prefix_chunk - 1) / p.prefix_chunk;
+    }
+  }
+  const int pieces = np + no;
+  const size_t row0 = size_t(r) * p.Hq + g * G;
+  // piece k of head h: its place among the prefix kernel's rows, or among the pieces
+  auto in_pre = [&](int k) { return p.pre_o != nullptr && k < np; };
+  auto at_piece = [&](int h, int k) { return (row0 + h) * p.parts + (k < np ? k : p.prefix_parts + k - np); };
+
+  for (int h = warp_id(); h < G; h += 8) {
+    const int lane = lane_id();
     float M = -INFINITY, W = 0.f;
-    for (int k = 0; k < no; ++k) M = fmaxf(M, pl[k]);
-    for (int k = 0; k < no; ++k) W += ex2(pl[k] - M);
-    s_lse[threadIdx.x] = M + __log2f(W);
+    for (int k = lane; k < pieces; k += 32) {
+      const float v = in_pre(k) ? p.pre_lse[pre0 + h + k * PRE_STEP] : p.part_lse[at_piece(h, k)];
+      s_w[h][k] = v;
+      M = fmaxf(M, v);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    for (int k = lane; k < pieces; k += 32) W += ex2(s_w[h][k] - M);  // (NaN where a wait ran out)
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) W += __shfl_xor_sync(0xffffffffu, W, m);
+    const float lse = pieces > 0 ? M + __log2f(W) : -INFINITY;  // no key at all: o = 0, lse = -inf
+    for (int k = lane; k < pieces; k += 32) s_w[h][k] = ex2(s_w[h][k] - lse);
+    if (lane == 0) s_lse[h] = lse;
   }
   __syncthreads();
-  const int s = blockIdx.x * 256 + threadIdx.x;
-  if (s >= n) return;
-  const size_t M = size_t(p.max_blocks) * part::BS;
-  const float* sc = p.scores + (size_t(r) * p.Hq + g * G) * M + s;
-  float w = 0.f;
-  for (int h = 0; h < G; ++h) w += ex2(sc[h * M] - s_lse[h]);
-  p.weights[(size_t(r) * p.Hkv + g) * M + s] += w;
+  if (join) {
+    constexpr int Q = D / 4;
+    for (int i = threadIdx.x; i < G * Q; i += 256) {
+      const int h = i / Q, c = (i % Q) * 4;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int k = 0; k < pieces; ++k) {
+        const float* src = in_pre(k) ? p.pre_o + (pre0 + h + k * PRE_STEP) * D : p.part_o + at_piece(h, k) * D;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + c));
+        const float w = s_w[h][k];
+        u.x += w * v.x;
+        u.y += w * v.y;
+        u.z += w * v.z;
+        u.w += w * v.w;
+      }
+      *reinterpret_cast<uint2*>(p.o + (row0 + h) * D + c) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
+    }
+    if (p.lse && int(threadIdx.x) < G) p.lse[row0 + threadIdx.x] = s_lse[threadIdx.x] * 0.69314718055994531f;
+    return;
+  }
+  if constexpr (SCORED) {
+    const int s = blockIdx.x * JOIN_TOKENS + threadIdx.x * 4;
+    if (s >= n) return;
+    const size_t M = size_t(p.max_blocks) * BS;
+    float* out = p.weights + (size_t(r) * p.Hkv + g) * M + s;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int h = 0; h < G; ++h) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.scores + (row0 + h) * M + s));
+      const float lse = s_lse[h];
+      w.x += ex2(v.x - lse);
+      w.y += ex2(v.y - lse);
+      w.z += ex2(v.z - lse);
+      w.w += ex2(v.w - lse);
+    }
+    if (s + 4 <= n) {
+      const float4 old = *reinterpret_cast<const float4*>(out);
+      *reinterpret_cast<float4*>(out) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+    } else {
+      const float add[3] = {w.x, w.y, w.z};
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (s + i < n) out[i] += add[i];
+    }
+  }
 }
 
 }  // namespace fa

@@ -17,6 +17,7 @@
 #include "bwd_f32.cuh"
 #include "qk_norm_rope.cuh"
 #include "decode_part.cuh"
+#include "shared_prefix.cuh"
 #include "evict.cuh"
 
 #ifndef FA_FWD_D64_BN

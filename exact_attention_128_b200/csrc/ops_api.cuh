@@ -2,6 +2,12 @@
 // position rotation, the decode steps over pieces of the cache, and the eviction.  Included by
 // fa_api.cu, whose helpers (alignment, TMA descriptors, launches) it uses.
 #pragma once
+#ifndef FA_PART_PERSM
+#define FA_PART_PERSM 12
+#endif
+#ifndef FA_PREFIX_ROWS
+#define FA_PREFIX_ROWS 64
+#endif
 #ifndef FA_ROPE_PERSM
 #define FA_ROPE_PERSM 32
 #endif
@@ -127,33 +133,59 @@ fa_status rope_by_d(RopeParams& prm, int d, bool inter, cudaStream_t st) {
 // ---- decode over pieces
 
 // Blocks of a piece: enough pieces for a few CTAs on each of 148 SMs when `sets` sets of rows
-// walk `blocks` blocks each, at least part::MIN_CHUNK blocks a piece and at most 64 pieces.
+// walk `blocks` blocks each, at least part::MIN_CHUNK blocks a piece and at most MAX_PARTS pieces.
 int part_chunk(int64_t sets, int64_t blocks) {
-  const int64_t want = std::max<int64_t>(1, (148 * 4 + sets - 1) / sets);
-  const int64_t pieces = std::min<int64_t>(64, want);
+  const int64_t want = std::max<int64_t>(1, (148 * FA_PART_PERSM + sets - 1) / sets);
+  const int64_t pieces = std::min<int64_t>(part::MAX_PARTS, want);
   const int64_t c = std::max<int64_t>(part::MIN_CHUNK, (blocks + pieces - 1) / pieces);
   return int((c + part::WARPS - 1) / part::WARPS * part::WARPS);
 }
 
+// Rows per kv head from which the prefix goes to the tensor-core kernel, whose CTAs work on 256
+// rows at a time; below, 16-row pieces read the prefix again for each 16 rows.
+constexpr int kPrefixTensorRows = FA_PREFIX_ROWS;
+
 struct PartPlan {
   int chunk, prefix_chunk, own_parts, prefix_parts, row_tiles;
-  size_t off_lse, off_scores, bytes;
+  int RT, pairs, pre_parts;  // tensor-core prefix: requests per row tile, tile pairs, results per item
+  size_t off_lse, off_scores, off_pre_o, off_pre_lse, bytes;
 };
 
 PartPlan part_plan(int R, int Hq, int Hkv, int d, int max_blocks, int prefix_blocks, bool scored) {
   PartPlan n = {};
+  const int G = Hq / Hkv;
   n.chunk = part_chunk(int64_t(R) * Hkv, max_blocks);
   n.own_parts = (max_blocks + n.chunk - 1) / n.chunk;
-  if (prefix_blocks > 0) {
-    n.row_tiles = int((int64_t(R) * (Hq / Hkv) + part::ROWS - 1) / part::ROWS);
+  if (prefix_blocks > 0 && int64_t(R) * G >= kPrefixTensorRows && G <= part::ROWS) {
+    n.RT = 128 / G;
+    n.pairs = (R + 2 * n.RT - 1) / (2 * n.RT);
+    n.pre_parts = int((part::PREFIX_CTAS + int64_t(n.pairs) * Hkv - 1) / (int64_t(n.pairs) * Hkv)) + 1;
+  } else if (prefix_blocks > 0) {
+    n.row_tiles = int((int64_t(R) * G + part::ROWS - 1) / part::ROWS);
     n.prefix_chunk = part_chunk(int64_t(n.row_tiles) * Hkv, prefix_blocks);
     n.prefix_parts = (prefix_blocks + n.prefix_chunk - 1) / n.prefix_chunk;
   }
   const size_t rows = size_t(R) * Hq * (n.own_parts + n.prefix_parts);
   n.off_lse = align256(rows * d * sizeof(float));
   n.off_scores = n.off_lse + align256(rows * sizeof(float));
-  n.bytes = n.off_scores + (scored ? align256(size_t(R) * Hq * max_blocks * part::BS * sizeof(float)) : 0);
+  n.off_pre_o = n.off_scores + (scored ? align256(size_t(R) * Hq * max_blocks * part::BS * sizeof(float)) : 0);
+  const size_t pre_rows = size_t(n.pairs) * Hkv * n.pre_parts * 256;
+  n.off_pre_lse = n.off_pre_o + pre_rows * d * sizeof(float);
+  n.bytes = n.off_pre_lse + pre_rows * sizeof(float);
   return n;
+}
+
+// 3-D map of q [R, Hq, d] with a box of one row tile's heads and requests.
+bool make_map_rows(CUtensorMap* m, const void* q, int d, int Hq, int R, int G, int RT) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(Hq), cuuint64_t(R)};
+  cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(d) * 2 * cuuint64_t(Hq)};
+  cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(RT)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool part_sizes(int R, int Hq, int Hkv, int d, int max_blocks, int block_size) {
@@ -170,19 +202,39 @@ fa_status part_launch(const CUtensorMap& mk, const CUtensorMap& mv, const PartPa
 }
 
 template <int D>
-fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, const PartParams& prm, const PartPlan& n, bool scored,
+fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const PartParams& prm, const PartPlan& n,
+                        cudaStream_t st) {
+  using C = PrefixCfg<D>;
+  CUtensorMap mq;
+  const int G = prm.Hq / prm.Hkv;
+  if (!make_map_rows(&mq, prm.q, D, prm.Hq, prm.R, G, n.RT)) return FA_ERR_CUDA;
+  const PrefixParams pp{prm.pbt, prm.plen, const_cast<float*>(prm.pre_o), const_cast<float*>(prm.pre_lse), prm.R,
+                        prm.Hkv, G, n.RT, n.pairs * prm.Hkv, n.pairs, n.pre_parts, prm.prefix_blocks, prm.num_blocks,
+                        prm.scale_log2, prm.wait_ns};
+  if (set_smem(fa_prefix_kernel<D>, C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_pdl(fa_prefix_kernel<D>, dim3(part::PREFIX_CTAS), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, pp) !=
+      cudaSuccess)
+    return FA_ERR_CUDA;
+  return FA_OK;
+}
+
+template <int D>
+fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm, const PartPlan& n, bool scored,
                    cudaStream_t st) {
   fa_status s = FA_OK;
-  if (prm.pbt) s = part_launch<D, true, false>(mk, mv, prm, dim3(n.prefix_parts, prm.Hkv, n.row_tiles), st);
+  if (prm.pre_o) {
+    s = prefix_launch<D>(mk, mv, prm, n, st);
+    prm.late_wait = true;
+  } else if (prm.pbt) {
+    s = part_launch<D, true, false>(mk, mv, prm, dim3(n.prefix_parts, prm.Hkv, n.row_tiles), st);
+  }
   if (s != FA_OK) return s;
   const dim3 own(n.own_parts, prm.Hkv, prm.R);
   s = scored ? part_launch<D, false, true>(mk, mv, prm, own, st) : part_launch<D, false, false>(mk, mv, prm, own, st);
   if (s != FA_OK) return s;
-  if (scored && launch_pdl(fa_decode_weights_kernel, dim3((prm.max_blocks * part::BS + 255) / 256, prm.Hkv, prm.R),
-                           dim3(256), 0, st, prm) != cudaSuccess)
-    return FA_ERR_CUDA;
-  if (launch_pdl(fa_decode_merge_kernel<D>, dim3(unsigned(prm.R * prm.Hq)), dim3(D), 0, st, prm) != cudaSuccess)
-    return FA_ERR_CUDA;
+  const unsigned x = scored ? (prm.max_blocks * part::BS + part::JOIN_TOKENS - 1) / part::JOIN_TOKENS + 1 : 1;
+  auto join = scored ? fa_decode_join_kernel<D, true> : fa_decode_join_kernel<D, false>;
+  if (launch_pdl(join, dim3(x, prm.Hkv, prm.R), dim3(256), 0, st, prm) != cudaSuccess) return FA_ERR_CUDA;
   return launched();
 }
 
@@ -215,7 +267,10 @@ fa_status part_call(const void* q, const void* k_cache, const void* v_cache, con
                  reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + n.off_lse),
                  reinterpret_cast<float*>(ws + n.off_scores), weights, block_table, ctx_lens, prefix_table, prefix_len,
                  R, Hq, Hkv, max_blocks, max_prefix_blocks, num_blocks, n.own_parts + n.prefix_parts, n.prefix_parts,
-                 n.chunk, n.prefix_chunk, scale * 1.4426950408889634f, g_wait_ns};
+                 n.chunk, n.prefix_chunk,
+                 n.pairs > 0 ? reinterpret_cast<const float*>(ws + n.off_pre_o) : nullptr,
+                 n.pairs > 0 ? reinterpret_cast<const float*>(ws + n.off_pre_lse) : nullptr,
+                 n.pre_parts, n.pairs, n.RT, false, scale * 1.4426950408889634f, g_wait_ns};
   CUtensorMap mk, mv;
   const long cache_rows = long(num_blocks) * Hkv * part::BS;
   if (!make_map_cache(&mk, k_cache, cache_rows, d) || !make_map_cache(&mv, v_cache, cache_rows, d)) return FA_ERR_CUDA;
@@ -385,7 +440,7 @@ size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int 
 fa_status fa_paged_decode_scored(const fa_paged_decode_scored_args* args, void* stream) {
   if (!args) return FA_ERR_INVALID_ARG;
   const fa_paged_decode_scored_args& a = *args;
-  if (!a.weights || !aligned(a.weights, 4)) return FA_ERR_INVALID_ARG;
+  if (!a.weights || !aligned(a.weights, 16)) return FA_ERR_INVALID_ARG;
   const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
                                  a.d, a.block_size,
                                  a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);

@@ -1,0 +1,374 @@
+// shared_prefix.cuh — the prefix part of a decode step of many requests, on the tensor cores.
+//
+// Requests that share a prefix turn its attention into a matrix product: the R * G query rows of a
+// kv head (request-major, G = Hq / Hkv heads each) against the prefix's P keys, with the
+// online-softmax recurrence over tiles of BN keys (running maximum m, sum l, numerator u).  Each
+// K/V block is read once per 256 rows.  What is left is one partial result (u / l, lse) per row
+// and run of tiles, merged by their mass with the requests' own tokens (decode_part.cuh).
+//
+// Work: an item is (kv head, two row tiles); a row tile is the most whole requests that fit 128
+// rows, so that one TMA box {64 columns, G heads, requests} fills it.  Items all have the same
+// nt = ceil(P / BN) key tiles, and CTA c of C takes tiles [c W / C, (c + 1) W / C) of all W =
+// items * nt: every CTA does the same work, whatever the batch and the prefix (P is read on the
+// device), and an item's tiles fall to a few consecutive CTAs, one partial result each.
+//   warp 0     producer (whole warp): Q by TMA per item; lane i < BN / 16 looks block i of a K/V
+//              tile up in the prefix table and issues its 16-row boxes.
+//   warp 1     MMA issuer: S_t = Q_t K^T into TMEM, then u_t += P_t V with P_t read from TMEM.
+//   warps 2-9  softmax of row tiles 0 and 1, one thread per row; while one tile's exponentials
+//              run, the tensor core works on the other tile.
+// BN = 64 and two K/V stages keep the CTA at 150 KB of shared memory and 320 threads of at most
+// 104 registers, so that a CTA of the requests' own (memory-bound) part runs on the SM beside it.
+// P is rounded to bf16 for P V: with many rows the tensor core is what bounds this part, and the
+// second product that would carry P's rest would cost it half as much again.
+#pragma once
+#include "decode_part.cuh"
+
+namespace fa {
+
+template <int D>
+struct PrefixCfg {
+  static constexpr int BM = 128, BN = PrefixDeal::BN;
+  static constexpr int KB = D / 64;
+  static constexpr int Q_TILE = BM * D * 2, KV_TILE = BN * D * 2;
+  static constexpr int NSTAGE = D == 128 ? 2 : 4;
+  static constexpr int STG_WARP = 32 * 16 * 4;  // epilogue staging of a warp: 32 rows x 16 columns fp32
+  static constexpr int OFF_Q = 0, OFF_K = 2 * Q_TILE, OFF_V = OFF_K + NSTAGE * KV_TILE;
+  static constexpr int OFF_STG = OFF_V + NSTAGE * KV_TILE, OFF_BAR = OFF_STG + 8 * STG_WARP;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + barriers, alignment of the base
+  static constexpr int THREADS = 320;
+  static constexpr uint32_t TMEM_COLS = D == 128 ? 512 : 256;
+  static constexpr uint32_t COL_S = 0, COL_O = 2 * BN;  // S_t at t * BN, u_t at t * D
+};
+
+struct PrefixParams {
+  const int *pbt, *plen;
+  float* part_o;    // [items][parts][2 tiles][128 rows][D]
+  float* part_lse;  // [items][parts][2][128], base 2
+  int R, Hkv, G, RT;  // RT requests per row tile
+  int items, pairs;   // items = Hkv * pairs, kv-head-major
+  int parts;
+  int prefix_blocks, num_blocks;
+  float scale_log2;
+  uint64_t wait_ns;
+};
+
+struct PrefixBars {
+  uint64_t q_full, q_empty, k_full[4], v_full[4], kv_empty[4], s_full[2], p_full[2], o_final[2], drained;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int D>
+__global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
+    fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p) {
+  using C = PrefixCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PrefixBars* bars = reinterpret_cast<PrefixBars*>(smem + C::OFF_BAR);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < C::NSTAGE; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 4);
+      mbar_init(&bars->o_final[t], 1);
+    }
+    mbar_init(&bars->drained, 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the grid after this one (the requests' own tokens) needs nothing of it and may start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int P = p.plen[0];
+  if (P < 0 || P > p.prefix_blocks * 16) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(FA_ERR_INVALID_ARG, 302);
+    P = 0;
+  }
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
+  const PrefixDeal deal(P, p.items);
+  const bool any = P > 0 && int(blockIdx.x) < deal.ctas;
+  const long long x0 = any ? deal.begin(blockIdx.x) : 0, x1 = any ? deal.begin(blockIdx.x + 1) : 0;
+  const int nblk = (P + 15) / 16;
+
+  if (warp == 0) {
+    constexpr int NB = C::BN / 16;
+    if (lane == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    int kv = 0, local = 0;
+    bool ok = true;
+    for (long long x = x0; x < x1 && ok; ++local) {
+      const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
+      const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
+      x += j1 - j0;
+      const int hk = it / p.pairs, pair = it - hk * p.pairs;
+      if (local > 0 && !(ok = warp_wait(&bars->q_empty, (local - 1) & 1, p.wait_ns, abort_flag, 311))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->q_full, uint32_t(2 * C::KB * 128 * p.G * p.RT));
+        for (int t = 0; t < 2; ++t)
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_3d(smem + C::OFF_Q + t * C::Q_TILE + kb * C::BM * 128, &tmQ, &bars->q_full, kb * 64, hk * p.G,
+                        (2 * pair + t) * p.RT);
+      }
+      int ph = (lane < NB && j0 * NB + lane < nblk) ? __ldg(p.pbt + j0 * NB + lane) : 0;
+      for (int j = j0; j < j1; ++j, ++kv) {
+        const int st = kv % C::NSTAGE, round = kv / C::NSTAGE;
+        const int lb = j * NB + lane;
+        const int ph_next = (lane < NB && j + 1 < j1 && lb + NB < nblk) ? __ldg(p.pbt + lb + NB) : 0;
+        if (round > 0 && !(ok = warp_wait(&bars->kv_empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 310))) break;
+        uint8_t* sk = smem + C::OFF_K + st * C::KV_TILE;
+        uint8_t* sv = smem + C::OFF_V + st * C::KV_TILE;
+        const int nload = min(NB, nblk - j * NB);  // >= 1
+        if (nload < NB) {  // V rows of blocks past the prefix: zero (their P is 0; 0 * NaN would not be)
+          for (int kb = 0; kb < C::KB; ++kb)
+            for (int i = nload * 128 + lane; i < C::BN * 8; i += 32)
+              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bytes = uint32_t(nload) * 16 * 128 * C::KB;
+          mbar_arrive_expect_tx(&bars->k_full[st], bytes);
+          mbar_arrive_expect_tx(&bars->v_full[st], bytes);
+        }
+        __syncwarp();
+        if (lane < nload) {
+          int pb = ph;
+          if (pb < 0 || pb >= p.num_blocks) {
+            set_status(FA_ERR_INVALID_ARG, 301);
+            pb = 0;
+          }
+          const int crow = (pb * p.Hkv + hk) * 16;
+          for (int kb = 0; kb < C::KB; ++kb) {
+            tma_load_2d(smem_u32(sk + kb * C::BN * 128 + lane * 16 * 128), &tmK, &bars->k_full[st], kb * 64, crow);
+            tma_load_2d(smem_u32(sv + kb * C::BN * 128 + lane * 16 * 128), &tmV, &bars->v_full[st], kb * 64, crow);
+          }
+        }
+        ph = ph_next;
+      }
+    }
+    if (!ok && lane == 0) {  // a wait ran out: let the loads in flight land before the CTA ends
+      for (int i = max(0, kv - C::NSTAGE); i < kv; ++i) {
+        mbar_wait_bounded(&bars->k_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
+        mbar_wait_bounded(&bars->v_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
+      }
+      if (local > 0) mbar_wait_bounded(&bars->q_full, (local - 1) & 1, p.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idS = idesc_bf16_f32(128, C::BN, 0), idPV = idesc_bf16_f32(128, D, 1);
+    const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dK = sdesc_sw128(sK, 16, 1024);
+    const uint64_t dV = sdesc_sw128(sV, C::BN * 128, 1024);
+    auto issue_S = [&](int t, int st) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int kb = ks >> 2, kin = ks & 3;
+        mma_ss_p(tmem + C::COL_S + t * C::BN, desc_add(dQ, t * C::Q_TILE + kb * C::BM * 128 + kin * 32),
+                 desc_add(dK, st * C::KV_TILE + kb * C::BN * 128 + kin * 32), idS, ks > 0 ? 1u : 0u, leader);
+      }
+    };
+    auto issue_PV = [&](int t, int st, bool first) {
+#pragma unroll
+      for (int ks = 0; ks < C::BN / 16; ++ks)
+        mma_ts_p(tmem + C::COL_O + t * D, tmem + C::COL_S + t * C::BN + ks * 8,
+                 desc_add(dV, st * C::KV_TILE + ks * 16 * 128), idPV, (!first || ks > 0) ? 1u : 0u, leader);
+    };
+    int kv = 0, g = 0, local = 0;
+    bool ok = true;
+    for (long long x = x0; x < x1 && ok; ++local) {
+      const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
+      const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
+      x += j1 - j0;
+      ok = warp_wait(&bars->q_full, local & 1, p.wait_ns, abort_flag, 320) &&
+           warp_wait(&bars->k_full[kv % C::NSTAGE], (kv / C::NSTAGE) & 1, p.wait_ns, abort_flag, 321);
+      if (!ok) break;
+      tc_fence_after();
+      issue_S(0, kv % C::NSTAGE);
+      mma_commit_p(&bars->s_full[0], leader);
+      issue_S(1, kv % C::NSTAGE);
+      mma_commit_p(&bars->s_full[1], leader);
+      if (j1 - j0 == 1) mma_commit_p(&bars->q_empty, leader);
+      for (int j = j0; j < j1; ++j, ++kv, ++g) {
+        const int st = kv % C::NSTAGE, st2 = (kv + 1) % C::NSTAGE;
+        const bool more = j + 1 < j1;
+        if (!(ok = warp_wait(&bars->v_full[st], (kv / C::NSTAGE) & 1, p.wait_ns, abort_flag, 322))) break;
+        if ((P & 15) != 0 && (P - 1) / C::BN == j) {  // V rows of the last block's unused slots: zero
+          uint8_t* sv = smem + C::OFF_V + st * C::KV_TILE;
+          const int r0 = P - j * C::BN, r1 = nblk * 16 - j * C::BN;
+          for (int kb = 0; kb < C::KB; ++kb)
+            for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!(ok = warp_wait(&bars->p_full[0], g & 1, p.wait_ns, abort_flag, 323))) break;
+        tc_fence_after();
+        issue_PV(0, st, j == j0);
+        if (more) {
+          if (!(ok = warp_wait(&bars->k_full[st2], ((kv + 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag, 324))) break;
+          tc_fence_after();
+          issue_S(0, st2);
+          mma_commit_p(&bars->s_full[0], leader);
+        } else {
+          mma_commit_p(&bars->o_final[0], leader);
+        }
+        if (!(ok = warp_wait(&bars->p_full[1], g & 1, p.wait_ns, abort_flag, 325))) break;
+        tc_fence_after();
+        issue_PV(1, st, j == j0);
+        mma_commit_p(&bars->kv_empty[st], leader);
+        if (more) {
+          issue_S(1, st2);
+          mma_commit_p(&bars->s_full[1], leader);
+          if (j + 2 == j1) mma_commit_p(&bars->q_empty, leader);  // that was the item's last S
+        } else {
+          mma_commit_p(&bars->o_final[1], leader);
+        }
+      }
+    }
+    if (!ok) {  // likewise the MMAs, before TMEM is given back
+      mma_commit_p(&bars->drained, leader);
+      if (lane == 0) mbar_wait_bounded(&bars->drained, 0, p.wait_ns);
+      __syncwarp();
+    }
+  } else {
+    const int t = (warp - 2) >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;  // row of the tile == TMEM lane
+    const uint32_t lane_off = uint32_t(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::COL_S + t * C::BN, tO = tmem + lane_off + C::COL_O + t * D;
+    const float sl2 = p.scale_log2;
+    int g = 0, local = 0;
+    bool ok = true;
+    for (long long x = x0; x < x1 && ok; ++local) {
+      const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
+      const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
+      x += j1 - j0;
+      const int req = (2 * (it % p.pairs) + t) * p.RT + r / p.G;
+      const bool idle = __all_sync(0xffffffffu, r >= p.G * p.RT || req >= p.R);
+      float m = -INFINITY, l = 0.f;
+      for (int j = j0; j < j1; ++j, ++g) {
+        if (!(ok = warp_wait(&bars->s_full[t], g & 1, p.wait_ns, abort_flag, 330 + t))) break;
+        if (!idle) {
+          tc_fence_after();
+          uint32_t sr[C::BN];
+#pragma unroll
+          for (int c = 0; c < C::BN / 32; ++c)
+            tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_wait_ld();
+          float f[C::BN];
+#pragma unroll
+          for (int c = 0; c < C::BN; ++c) f[c] = __uint_as_float(sr[c]);
+          const int lim = P - j * C::BN;
+          if (lim < C::BN) {
+#pragma unroll
+            for (int c = 0; c < C::BN; ++c) f[c] = (c < lim) ? f[c] : -INFINITY;
+          }
+          float mx8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(f[k], f[8 + k]);
+#pragma unroll
+          for (int c = 16; c < C::BN; c += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], f[c + k], f[c + 8 + k]);
+          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmaxf(fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          // the reference of l and u moves only when the maximum passes it by FA_RESCALE_LOG2 (see the forward kernel)
+          const float m_cand = fmaxf(m, mx * sl2);
+          const float m_new = (m_cand > m + FA_RESCALE_LOG2) ? m_cand : m;
+          const float base = (m_new == -INFINITY) ? 0.f : m_new;
+          const float alpha = (m_new == m) ? 1.f : ex2(m - base);
+          const float2 sl2v = make_float2(sl2, sl2), nbase = make_float2(-base, -base);
+          float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < C::BN / 32; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = __ffma2_rn(make_float2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), sl2v, nbase);
+              const float2 pv = make_float2(ex2(y.x), ex2(y.y));
+              rs2[i & 3] = __fadd2_rn(rs2[i & 3], pv);
+              pk[i] = pack_bf16x2(pv.x, pv.y);
+            }
+            tmem_st16(tS + c * 16, pk);
+          }
+          const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
+          l = l * alpha + (rsa.x + rsa.y);
+          if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+          m = m_new;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+      }
+      if (ok) ok = warp_wait(&bars->o_final[t], local & 1, p.wait_ns, abort_flag, 340 + t);
+      if (!ok) break;
+      if (idle) continue;
+      tc_fence_after();
+      // u / l: 16 columns at a time through the warp's staging (16-byte pieces swizzled by the row),
+      // so that four lanes write 64 consecutive bytes of a row
+      const float inv = 1.f / l;
+      const int part = int(blockIdx.x) - deal.owner((long long)(it)*deal.nt);
+      const size_t row0 = ((size_t(it) * p.parts + part) * 2 + t) * C::BM + wq * 32;
+      uint8_t* stg = smem + C::OFF_STG + (warp - 2) * C::STG_WARP;
+#pragma unroll 2
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(tO + c * 16, o);
+        tmem_wait_ld();
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<float4*>(stg + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+              make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                          __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = k * 8 + (lane >> 2), u = lane & 3;
+          *reinterpret_cast<float4*>(p.part_o + (row0 + rr) * D + c * 16 + u * 4) =
+              *reinterpret_cast<const float4*>(stg + rr * 64 + ((u ^ ((rr >> 1) & 3)) << 4));
+        }
+      }
+      p.part_lse[row0 + lane] = m + __log2f(l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace fa

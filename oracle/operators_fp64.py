@@ -88,6 +88,7 @@ def _decode(q, keys, values, scale):
 
 def decode_shared(q, k_cache, v_cache, prefix_table, prefix_len, block_table, ctx_lens, block_size, scale):
     q, table = to_f64(q), np.asarray(block_table)
+    k_cache, v_cache = to_f64(k_cache), to_f64(v_cache)
     Hkv, P = k_cache.shape[1], int(prefix_len)
     pre = [[depage(c, np.asarray(prefix_table), P, g, block_size) for g in range(Hkv)] for c in (k_cache, v_cache)]
     o, lse = np.empty_like(q), np.empty(q.shape[:2])
@@ -100,6 +101,7 @@ def decode_shared(q, k_cache, v_cache, prefix_table, prefix_len, block_table, ct
 
 def decode_scored(q, k_cache, v_cache, block_table, ctx_lens, weights, block_size, scale):
     q, table, w = to_f64(q), np.asarray(block_table), to_f64(weights).copy()
+    k_cache, v_cache = to_f64(k_cache), to_f64(v_cache)
     o, lse = np.empty_like(q), np.empty(q.shape[:2])
     for r, n in enumerate(np.asarray(ctx_lens)):
         kv = [[depage(c, table[r], int(n), g, block_size) for g in range(k_cache.shape[1])] for c in (k_cache, v_cache)]

@@ -28,7 +28,8 @@ HALF = {BF: 2.0**-8, F32: 2.0**-24}
 def near(got, ref, slack, what=""):
     """|got - ref| <= half a step of ref + slack, elementwise."""
     g = got.detach().double().cpu().numpy()
-    off = np.abs(g - ref) - (HALF.get(got.dtype, 0) * np.abs(ref) * (1 + 2.0**-6) + slack)
+    with np.errstate(invalid="ignore"):  # -inf against -inf
+        off = np.abs(g - ref) - (HALF.get(got.dtype, 0) * np.abs(ref) * (1 + 2.0**-6) + slack)
     same_inf = np.isinf(ref) & (g == ref)
     off = np.where(same_inf, 0.0, off)
     worst = off.max(initial=-1.0)
@@ -289,6 +290,12 @@ def decode_case(lens, Hq, Hkv, d, maxb, seed, prefix=0):
         (6, 2, 47, tuple(range(50))),
         (8, 1, 1040, tuple(i % 3 for i in range(70))),
         (3, 1, 5000, (600, 1)),
+        (5, 1, 65, tuple(i % 20 for i in range(40))),  # 25 requests of 5 heads fill 125 of a tile's 128 rows
+        (16, 16, 190, tuple(i % 2 for i in range(70))),
+        (16, 1, 1, (0,) * 9),
+        (8, 4, 64, (1,) * 150),
+        (14, 2, 3333, (0, 5) * 30),
+        (4, 1, 16, (2,) * 16),
     ],
 )
 def test_decode_shared(d, Hq, Hkv, prefix, lens):
@@ -298,7 +305,9 @@ def test_decode_shared(d, Hq, Hkv, prefix, lens):
     clean()
     O, L = ops.decode_shared(q, kc, vc, ptable, prefix, table, ctx, 16, d**-0.5)
     delta, slack = bounds(q, kc, vc, d**-0.5)
-    near(o, O, slack + 2.0**-8 * np.abs(O).max(), "o")
+    # with many rows P is rounded to bf16: sum p 2^-8 |v| at most, an attention over |v|
+    V, _ = ops.decode_shared(q, kc, vc.abs(), ptable, prefix, table, ctx, 16, d**-0.5)
+    near(o, O, slack + 2.0**-8 * V, "o")
     near(lse, L, delta + 2.0**-20 * np.abs(np.where(np.isinf(L), 0, L)), "lse")
     again, _ = fa.paged_decode_shared(*dev, with_lse=False)
     assert torch.equal(o, again)
