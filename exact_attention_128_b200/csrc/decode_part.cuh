@@ -26,7 +26,7 @@ constexpr int ROWS = 16;       // query rows of a piece
 constexpr int MIN_CHUNK = 8;   // blocks of a piece, at least: two for each warp
 constexpr int MAX_PARTS = 64;  // pieces of a row, at most, of either kind
 constexpr int PREFIX_CTAS = 148;  // CTAs of the tensor-core prefix kernel, at most
-constexpr int JOIN_TOKENS = 1024;  // tokens whose weights one CTA adds up
+constexpr int JOIN_TOKENS = 1024;  // tokens whose weights one CTA adds up at a time
 
 template <int D>
 struct Cfg {
@@ -345,101 +345,151 @@ struct PrefixDeal {
   __device__ int owner(long long x) const { return int(((x + 1) * ctas - 1) / all); }
 };
 
-// Joins the pieces of the G rows of (request, kv head).  The last CTA of x writes o and lse; SCORED:
-// the others add up the weights of JOIN_TOKENS tokens each,
-//   weights[r, g, s] += sum over the heads of kv head g of e^{score - lse}.
-template <int D, bool SCORED>
-__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ PartParams p) {
-  using namespace part;
-  __shared__ float s_w[ROWS][MAX_PARTS + PREFIX_CTAS + 1];  // pieces' lse, then their weights
-  __shared__ float s_lse[ROWS];
-  const int g = blockIdx.y, r = blockIdx.z, G = p.Hq / p.Hkv;
-  const bool join = blockIdx.x == gridDim.x - 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = p.ctx[r], P = p.plen ? p.plen[0] : 0;
-  const bool bad = n < 0 || n > p.max_blocks * BS || P < 0 || P > p.prefix_blocks * BS;
-  if (SCORED && !join && (bad || int(blockIdx.x) * JOIN_TOKENS >= n)) return;
-  const int no = bad ? 0 : ((n + BS - 1) / BS + p.chunk - 1) / p.chunk;
-  int np = 0;
-  size_t pre0 = 0;  // first row of the prefix kernel's results for these rows, and their distance
-  constexpr size_t PRE_STEP = 256;
-  if (!bad && P > 0) {
+// The pieces of the rows of (request r, kv head g): `np` of the prefix and `no` of its own tokens.
+struct PartPieces {
+  int np, no;
+  size_t pre0;  // first row of the prefix kernel's results for these heads; 256 rows to the next piece
+  __device__ PartPieces(const PartParams& p, int r, int g, int n) {
+    using namespace part;
+    const int P = p.plen ? p.plen[0] : 0;
+    const bool bad = n < 0 || n > p.max_blocks * BS || P < 0 || P > p.prefix_blocks * BS;
+    no = bad ? 0 : ((n + BS - 1) / BS + p.chunk - 1) / p.chunk;
+    np = 0;
+    pre0 = 0;
+    if (bad || P == 0) return;
     if (p.pre_o) {
       const int tile = r / p.RT, it = g * p.pairs + tile / 2;
       const PrefixDeal deal(P, p.Hkv * p.pairs);
       np = deal.owner((long long)(it + 1) * deal.nt - 1) - deal.owner((long long)(it)*deal.nt) + 1;
-      pre0 = (size_t(it) * p.pre_parts * 2 + (tile & 1)) * 128 + (r - tile * p.RT) * G;
+      pre0 = (size_t(it) * p.pre_parts * 2 + (tile & 1)) * 128 + (r - tile * p.RT) * (p.Hq / p.Hkv);
     } else {
       np = ((P + BS - 1) / BS + p.prefix_chunk - 1) / p.prefix_chunk;
     }
   }
-  const int pieces = np + no;
-  const size_t row0 = size_t(r) * p.Hq + g * G;
-  // piece k of head h: its place among the prefix kernel's rows, or among the pieces
-  auto in_pre = [&](int k) { return p.pre_o != nullptr && k < np; };
-  auto at_piece = [&](int h, int k) { return (row0 + h) * p.parts + (k < np ? k : p.prefix_parts + k - np); };
-
-  for (int h = warp_id(); h < G; h += 8) {
-    const int lane = lane_id();
-    float M = -INFINITY, W = 0.f;
-    for (int k = lane; k < pieces; k += 32) {
-      const float v = in_pre(k) ? p.pre_lse[pre0 + h + k * PRE_STEP] : p.part_lse[at_piece(h, k)];
-      s_w[h][k] = v;
-      M = fmaxf(M, v);
-    }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    for (int k = lane; k < pieces; k += 32) W += ex2(s_w[h][k] - M);  // (NaN where a wait ran out)
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) W += __shfl_xor_sync(0xffffffffu, W, m);
-    const float lse = pieces > 0 ? M + __log2f(W) : -INFINITY;  // no key at all: o = 0, lse = -inf
-    for (int k = lane; k < pieces; k += 32) s_w[h][k] = ex2(s_w[h][k] - lse);
-    if (lane == 0) s_lse[h] = lse;
+  // piece k of head h of the group, as a row of the prefix kernel's results or of the pieces
+  __device__ bool in_pre(const PartParams& p, int k) const { return p.pre_o != nullptr && k < np; }
+  __device__ size_t row(const PartParams& p, size_t row0, int h, int k) const {
+    if (in_pre(p, k)) return pre0 + h + size_t(k) * 256;
+    return (row0 + h) * p.parts + (k < np ? k : p.prefix_parts + k - np);
   }
-  __syncthreads();
-  if (join) {
-    constexpr int Q = D / 4;
-    for (int i = threadIdx.x; i < G * Q; i += 256) {
-      const int h = i / Q, c = (i % Q) * 4;
-      float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+};
+
+// One warp: lse (base 2) of head h's row from its pieces; w[k] becomes piece k's share e^{lse_k - lse}.
+__device__ __forceinline__ float part_lse_of(const PartParams& p, const PartPieces& x, size_t row0, int h, float* w) {
+  const int lane = lane_id(), pieces = x.np + x.no;
+  float M = -INFINITY, W = 0.f;
+  for (int k = lane; k < pieces; k += 32) {
+    const float v = (x.in_pre(p, k) ? p.pre_lse : p.part_lse)[x.row(p, row0, h, k)];
+    w[k] = v;
+    M = fmaxf(M, v);
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+  for (int k = lane; k < pieces; k += 32) W += ex2(w[k] - M);  // (NaN where a wait ran out)
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) W += __shfl_xor_sync(0xffffffffu, W, m);
+  const float lse = pieces > 0 ? M + __log2f(W) : -INFINITY;  // no key at all: o = 0, lse = -inf
+  for (int k = lane; k < pieces; k += 32) w[k] = ex2(w[k] - lse);
+  __syncwarp();
+  return lse;
+}
+
+// The first `joins` CTAs write o and lse: `strands` of their eight warps share a row (request,
+// head), each adding up every strands-th piece.  SCORED: the others, `spans` for each (request, kv
+// head), add up the weights of JOIN_TOKENS tokens at a time,
+//   weights[r, g, s] += sum over the heads of kv head g of e^{score - lse}.
+template <int D, bool SCORED>
+__global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_constant__ PartParams p, int joins,
+                                                             int strands, int spans) {
+  using namespace part;
+  constexpr int PIECES = MAX_PARTS + PREFIX_CTAS + 1;
+  __shared__ float s_w[8][PIECES];
+  __shared__ float s_lse[ROWS];
+  __shared__ float4 s_u[8][D / 4];
+  const int G = p.Hq / p.Hkv, warp = warp_id(), lane = lane_id();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (int(blockIdx.x) < joins) {
+    const int row = blockIdx.x * (8 / strands) + warp / strands, strand = warp % strands;
+    const bool on = row < p.R * p.Hq;
+    constexpr int Q = D / 4, PER = 32 / Q;  // lanes of a row, pieces a warp reads at a time
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lse = 0.f;
+    if (on) {
+      const int r = row / p.Hq, h = row - r * p.Hq, g = h / G;
+      const PartPieces x(p, r, g, p.ctx[r]);
+      const size_t row0 = size_t(r) * p.Hq + g * G;
+      lse = part_lse_of(p, x, row0, h - g * G, s_w[warp]);
+      const int pieces = x.np + x.no, c = (lane % Q) * 4;
 #pragma unroll 8
-      for (int k = 0; k < pieces; ++k) {
-        const float* src = in_pre(k) ? p.pre_o + (pre0 + h + k * PRE_STEP) * D : p.part_o + at_piece(h, k) * D;
+      for (int k = strand * PER + lane / Q; k < pieces; k += strands * PER) {
+        const float* src = (x.in_pre(p, k) ? p.pre_o : p.part_o) + x.row(p, row0, h - g * G, k) * D;
         const float4 v = __ldcg(reinterpret_cast<const float4*>(src + c));
-        const float w = s_w[h][k];
+        const float w = s_w[warp][k];
         u.x += w * v.x;
         u.y += w * v.y;
         u.z += w * v.z;
         u.w += w * v.w;
       }
-      *reinterpret_cast<uint2*>(p.o + (row0 + h) * D + c) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
+      if constexpr (PER == 2) {
+        u.x += __shfl_xor_sync(0xffffffffu, u.x, 16);
+        u.y += __shfl_xor_sync(0xffffffffu, u.y, 16);
+        u.z += __shfl_xor_sync(0xffffffffu, u.z, 16);
+        u.w += __shfl_xor_sync(0xffffffffu, u.w, 16);
+      }
     }
-    if (p.lse && int(threadIdx.x) < G) p.lse[row0 + threadIdx.x] = s_lse[threadIdx.x] * 0.69314718055994531f;
+    if (strands > 1) {
+      if (lane < Q) s_u[warp][lane] = u;
+      __syncthreads();
+      if (strand == 0 && lane < Q)
+        for (int k = 1; k < strands; ++k) {
+          const float4 v = s_u[warp + k][lane];
+          u.x += v.x;
+          u.y += v.y;
+          u.z += v.z;
+          u.w += v.w;
+        }
+    }
+    if (on && strand == 0) {
+      if (lane < Q)
+        *reinterpret_cast<uint2*>(p.o + size_t(row) * D + lane * 4) =
+            make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
+      if (lane == 0 && p.lse) p.lse[row] = lse * 0.69314718055994531f;
+    }
     return;
   }
   if constexpr (SCORED) {
-    const int s = blockIdx.x * JOIN_TOKENS + threadIdx.x * 4;
-    if (s >= n) return;
-    const size_t M = size_t(p.max_blocks) * BS;
-    float* out = p.weights + (size_t(r) * p.Hkv + g) * M + s;
-    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int h = 0; h < G; ++h) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.scores + (row0 + h) * M + s));
-      const float lse = s_lse[h];
-      w.x += ex2(v.x - lse);
-      w.y += ex2(v.y - lse);
-      w.z += ex2(v.z - lse);
-      w.w += ex2(v.w - lse);
+    const int at = blockIdx.x - joins, set = at / spans, span = at - set * spans;
+    const int r = set / p.Hkv, g = set - r * p.Hkv;
+    const int n = p.ctx[r];
+    if (span * JOIN_TOKENS >= n) return;
+    const PartPieces x(p, r, g, n);
+    if (x.no == 0) return;  // a length out of range
+    const size_t row0 = size_t(r) * p.Hq + g * G, M = size_t(p.max_blocks) * BS;
+    for (int h = warp; h < G; h += 8) {
+      const float lse = part_lse_of(p, x, row0, h, s_w[warp]);
+      if (lane == 0) s_lse[h] = lse;
     }
-    if (s + 4 <= n) {
+    __syncthreads();
+    for (int s = span * JOIN_TOKENS + threadIdx.x * 4; s < n; s += spans * JOIN_TOKENS) {
+      float* out = p.weights + (size_t(r) * p.Hkv + g) * M + s;
       const float4 old = *reinterpret_cast<const float4*>(out);
-      *reinterpret_cast<float4*>(out) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
-    } else {
-      const float add[3] = {w.x, w.y, w.z};
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (s + i < n) out[i] += add[i];
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int h = 0; h < G; ++h) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.scores + (row0 + h) * M + s));
+        const float lse = s_lse[h];
+        w.x += ex2(v.x - lse);
+        w.y += ex2(v.y - lse);
+        w.z += ex2(v.z - lse);
+        w.w += ex2(v.w - lse);
+      }
+      if (s + 4 <= n) {
+        *reinterpret_cast<float4*>(out) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+      } else {
+        out[0] = old.x + w.x;
+        if (s + 1 < n) out[1] = old.y + w.y;
+        if (s + 2 < n) out[2] = old.z + w.z;
+      }
     }
   }
 }

@@ -195,7 +195,10 @@ bool part_sizes(int R, int Hq, int Hkv, int d, int max_blocks, int block_size) {
 template <int D, bool PREFIX, bool SCORED>
 fa_status part_launch(const CUtensorMap& mk, const CUtensorMap& mv, const PartParams& prm, dim3 grid, cudaStream_t st) {
   auto kern = fa_decode_part_kernel<D, PREFIX, SCORED>;
-  if (set_smem(kern, part::Cfg<D>::SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  if (set_smem(kern, part::Cfg<D>::SMEM) != cudaSuccess ||
+      cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+          cudaSuccess)
+    return FA_ERR_CUDA;
   if (launch_pdl(kern, grid, dim3(part::WARPS * 32), part::Cfg<D>::SMEM, st, mk, mv, prm) != cudaSuccess)
     return FA_ERR_CUDA;
   return FA_OK;
@@ -211,7 +214,11 @@ fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const Part
   const PrefixParams pp{prm.pbt, prm.plen, const_cast<float*>(prm.pre_o), const_cast<float*>(prm.pre_lse), prm.R,
                         prm.Hkv, G, n.RT, n.pairs * prm.Hkv, n.pairs, n.pre_parts, prm.prefix_blocks, prm.num_blocks,
                         prm.scale_log2, prm.wait_ns};
-  if (set_smem(fa_prefix_kernel<D>, C::SMEM) != cudaSuccess) return FA_ERR_CUDA;
+  // (all of the SM's memory as shared memory: the CTA of the next grid has to find room beside this one)
+  if (set_smem(fa_prefix_kernel<D>, C::SMEM) != cudaSuccess ||
+      cudaFuncSetAttribute(fa_prefix_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+    return FA_ERR_CUDA;
   if (launch_pdl(fa_prefix_kernel<D>, dim3(part::PREFIX_CTAS), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, pp) !=
       cudaSuccess)
     return FA_ERR_CUDA;
@@ -224,7 +231,9 @@ fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm
   fa_status s = FA_OK;
   if (prm.pre_o) {
     s = prefix_launch<D>(mk, mv, prm, n, st);
+#ifndef FA_NO_LATE
     prm.late_wait = true;
+#endif
   } else if (prm.pbt) {
     s = part_launch<D, true, false>(mk, mv, prm, dim3(n.prefix_parts, prm.Hkv, n.row_tiles), st);
   }
@@ -232,9 +241,19 @@ fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm
   const dim3 own(n.own_parts, prm.Hkv, prm.R);
   s = scored ? part_launch<D, false, true>(mk, mv, prm, own, st) : part_launch<D, false, false>(mk, mv, prm, own, st);
   if (s != FA_OK) return s;
-  const unsigned x = scored ? (prm.max_blocks * part::BS + part::JOIN_TOKENS - 1) / part::JOIN_TOKENS + 1 : 1;
+  // warps that share a row of the join: one for each 8 pieces it may have
+  const int most = n.own_parts + n.prefix_parts + n.pre_parts;
+  const int strands = most > 32 ? 8 : most > 16 ? 4 : most > 8 ? 2 : 1;
+  const int64_t joins = (int64_t(prm.R) * prm.Hq * strands + 7) / 8;
+  const int64_t sets = int64_t(prm.R) * prm.Hkv;
+  // spans of weights: four CTAs for each SM in all, at most one per JOIN_TOKENS tokens
+  const int64_t spans = std::min<int64_t>((int64_t(prm.max_blocks) * part::BS + part::JOIN_TOKENS - 1) / part::JOIN_TOKENS,
+                                          std::max<int64_t>(1, 148 * 4 / sets));
+  const int64_t grid = joins + (scored ? sets * spans : 0);
+  if (grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
   auto join = scored ? fa_decode_join_kernel<D, true> : fa_decode_join_kernel<D, false>;
-  if (launch_pdl(join, dim3(x, prm.Hkv, prm.R), dim3(256), 0, st, prm) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_pdl(join, dim3(unsigned(grid)), dim3(256), 0, st, prm, int(joins), strands, int(spans)) != cudaSuccess)
+    return FA_ERR_CUDA;
   return launched();
 }
 

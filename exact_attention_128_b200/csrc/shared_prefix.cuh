@@ -14,8 +14,11 @@
 //   warp 0     producer (whole warp): Q by TMA per item; lane i < BN / 16 looks block i of a K/V
 //              tile up in the prefix table and issues its 16-row boxes.
 //   warp 1     MMA issuer: S_t = Q_t K^T into TMEM, then u_t += P_t V with P_t read from TMEM.
-//   warps 2-9  softmax of row tiles 0 and 1, one thread per row; while one tile's exponentials
-//              run, the tensor core works on the other tile.
+//   warps 2-9  softmax of row tiles 0 and 1, one thread per row.
+// Scores are double-buffered in TMEM and issued one key tile ahead, so a softmax warp goes from
+// one tile to the next without waiting for its own P V (with one buffer, the chain S, softmax,
+// P V of a 64-key tile took 3290 cycles a step of two row tiles; MMAs alone take about 1100).
+// Only the rare step whose maximum rises waits for the P V before it, to rescale u.
 // BN = 64 and two K/V stages keep the CTA at 150 KB of shared memory and 320 threads of at most
 // 104 registers, so that a CTA of the requests' own (memory-bound) part runs on the SM beside it.
 // P is rounded to bf16 for P V: with many rows the tensor core is what bounds this part, and the
@@ -36,8 +39,9 @@ struct PrefixCfg {
   static constexpr int OFF_STG = OFF_V + NSTAGE * KV_TILE, OFF_BAR = OFF_STG + 8 * STG_WARP;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + barriers, alignment of the base
   static constexpr int THREADS = 320;
-  static constexpr uint32_t TMEM_COLS = D == 128 ? 512 : 256;
-  static constexpr uint32_t COL_S = 0, COL_O = 2 * BN;  // S_t at t * BN, u_t at t * D
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t COL_O = 4 * BN;  // S of row tile t, buffer b at (2 b + t) * BN; u_t at COL_O + t * D
+  static_assert(4 * BN + 2 * D <= 512, "TMEM");
 };
 
 struct PrefixParams {
@@ -53,10 +57,13 @@ struct PrefixParams {
 };
 
 struct PrefixBars {
-  uint64_t q_full, q_empty, k_full[4], v_full[4], kv_empty[4], s_full[2], p_full[2], o_final[2], drained;
+  uint64_t q_full, q_empty, k_full[4], v_full[4], k_empty[4], v_empty[4];
+  uint64_t s_full[2][2], p_full[2][2];  // [row tile][buffer]
+  uint64_t pv_done[2], o_final[2], drained;
   uint32_t tmem_base;
   int abort_flag;
 };
+static_assert(sizeof(PrefixBars) <= 256, "barrier area");
 
 template <int D>
 __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
@@ -74,11 +81,15 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
     for (int s = 0; s < C::NSTAGE; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->kv_empty[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[t][b], 1);
+        mbar_init(&bars->p_full[t][b], 4);
+      }
+      mbar_init(&bars->pv_done[t], 1);
       mbar_init(&bars->o_final[t], 1);
     }
     mbar_init(&bars->drained, 1);
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
-    int kv = 0, local = 0;
+    int kv = 0, kv_k = 0, local = 0;  // V and K tiles issued
     bool ok = true;
     for (long long x = x0; x < x1 && ok; ++local) {
       const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
@@ -135,43 +146,46 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
         const int st = kv % C::NSTAGE, round = kv / C::NSTAGE;
         const int lb = j * NB + lane;
         const int ph_next = (lane < NB && j + 1 < j1 && lb + NB < nblk) ? __ldg(p.pbt + lb + NB) : 0;
-        if (round > 0 && !(ok = warp_wait(&bars->kv_empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 310))) break;
+        if (round > 0 && !(ok = warp_wait(&bars->k_empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 310))) break;
         uint8_t* sk = smem + C::OFF_K + st * C::KV_TILE;
         uint8_t* sv = smem + C::OFF_V + st * C::KV_TILE;
         const int nload = min(NB, nblk - j * NB);  // >= 1
-        if (nload < NB) {  // V rows of blocks past the prefix: zero (their P is 0; 0 * NaN would not be)
-          for (int kb = 0; kb < C::KB; ++kb)
-            for (int i = nload * 128 + lane; i < C::BN * 8; i += 32)
-              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t bytes = uint32_t(nload) * 16 * 128 * C::KB;
-          mbar_arrive_expect_tx(&bars->k_full[st], bytes);
-          mbar_arrive_expect_tx(&bars->v_full[st], bytes);
-        }
-        __syncwarp();
+        const uint32_t bytes = uint32_t(nload) * 16 * 128 * C::KB;
+        int crow = 0;
         if (lane < nload) {
           int pb = ph;
           if (pb < 0 || pb >= p.num_blocks) {
             set_status(FA_ERR_INVALID_ARG, 301);
             pb = 0;
           }
-          const int crow = (pb * p.Hkv + hk) * 16;
-          for (int kb = 0; kb < C::KB; ++kb) {
-            tma_load_2d(smem_u32(sk + kb * C::BN * 128 + lane * 16 * 128), &tmK, &bars->k_full[st], kb * 64, crow);
-            tma_load_2d(smem_u32(sv + kb * C::BN * 128 + lane * 16 * 128), &tmV, &bars->v_full[st], kb * 64, crow);
-          }
+          crow = (pb * p.Hkv + hk) * 16;
         }
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], bytes);
+        __syncwarp();
+        if (lane < nload)
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_2d(smem_u32(sk + kb * C::BN * 128 + lane * 16 * 128), &tmK, &bars->k_full[st], kb * 64, crow);
+        ++kv_k;
+        if (round > 0 && !(ok = warp_wait(&bars->v_empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 312))) break;
+        if (nload < NB) {  // V rows of blocks past the prefix: zero (their P is 0; 0 * NaN would not be)
+          for (int kb = 0; kb < C::KB; ++kb)
+            for (int i = nload * 128 + lane; i < C::BN * 8; i += 32)
+              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[st], bytes);
+        __syncwarp();
+        if (lane < nload)
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_2d(smem_u32(sv + kb * C::BN * 128 + lane * 16 * 128), &tmV, &bars->v_full[st], kb * 64, crow);
         ph = ph_next;
       }
     }
     if (!ok && lane == 0) {  // a wait ran out: let the loads in flight land before the CTA ends
-      for (int i = max(0, kv - C::NSTAGE); i < kv; ++i) {
+      for (int i = max(0, kv_k - C::NSTAGE); i < kv_k; ++i)
         mbar_wait_bounded(&bars->k_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
+      for (int i = max(0, kv - C::NSTAGE); i < kv; ++i)
         mbar_wait_bounded(&bars->v_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
-      }
       if (local > 0) mbar_wait_bounded(&bars->q_full, (local - 1) & 1, p.wait_ns);
     }
     __syncwarp();
@@ -180,22 +194,37 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
     constexpr uint32_t idS = idesc_bf16_f32(128, C::BN, 0), idPV = idesc_bf16_f32(128, D, 1);
     const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dK = sdesc_sw128(sK, 16, 1024);
     const uint64_t dV = sdesc_sw128(sV, C::BN * 128, 1024);
-    auto issue_S = [&](int t, int st) {
+    // scores of both row tiles against the K tile of ring position i, into the buffers of step g
+    auto issue_S = [&](int i, int g) {
+      const int st = i % C::NSTAGE;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const int kb = ks >> 2, kin = ks & 3;
-        mma_ss_p(tmem + C::COL_S + t * C::BN, desc_add(dQ, t * C::Q_TILE + kb * C::BM * 128 + kin * 32),
-                 desc_add(dK, st * C::KV_TILE + kb * C::BN * 128 + kin * 32), idS, ks > 0 ? 1u : 0u, leader);
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int kb = ks >> 2, kin = ks & 3;
+          mma_ss_p(tmem + (2 * (g & 1) + t) * C::BN, desc_add(dQ, t * C::Q_TILE + kb * C::BM * 128 + kin * 32),
+                   desc_add(dK, st * C::KV_TILE + kb * C::BN * 128 + kin * 32), idS, ks > 0 ? 1u : 0u, leader);
+        }
+        mma_commit_p(&bars->s_full[t][g & 1], leader);
       }
+      mma_commit_p(&bars->k_empty[st], leader);
     };
-    auto issue_PV = [&](int t, int st, bool first) {
+    auto issue_PV = [&](int t, int st, int g, bool first) {
 #pragma unroll
       for (int ks = 0; ks < C::BN / 16; ++ks)
-        mma_ts_p(tmem + C::COL_O + t * D, tmem + C::COL_S + t * C::BN + ks * 8,
+        mma_ts_p(tmem + C::COL_O + t * D, tmem + (2 * (g & 1) + t) * C::BN + ks * 8,
                  desc_add(dV, st * C::KV_TILE + ks * 16 * 128), idPV, (!first || ks > 0) ? 1u : 0u, leader);
+      mma_commit_p(&bars->pv_done[t], leader);
     };
-    int kv = 0, g = 0, local = 0;
+    int kv = 0, local = 0;  // kv: K/V tiles so far, which is also the step (every tile is one)
     bool ok = true;
+    // The scores of a step go where P of two steps before was.  The tensor core keeps the order of
+    // MMAs of one shape and accumulator only, so that step's P V must be waited for.  pv_done is
+    // waited for once per step, in order: a barrier two phases ahead would look incomplete.
+    auto pv_complete = [&](int s) {
+      return s < 0 || (warp_wait(&bars->pv_done[0], s & 1, p.wait_ns, abort_flag, 326) &&
+                       warp_wait(&bars->pv_done[1], s & 1, p.wait_ns, abort_flag, 327));
+    };
     for (long long x = x0; x < x1 && ok; ++local) {
       const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
       const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
@@ -204,14 +233,18 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
            warp_wait(&bars->k_full[kv % C::NSTAGE], (kv / C::NSTAGE) & 1, p.wait_ns, abort_flag, 321);
       if (!ok) break;
       tc_fence_after();
-      issue_S(0, kv % C::NSTAGE);
-      mma_commit_p(&bars->s_full[0], leader);
-      issue_S(1, kv % C::NSTAGE);
-      mma_commit_p(&bars->s_full[1], leader);
+      issue_S(kv, kv);  // (over P of step kv - 2, which was waited for before step kv - 1)
       if (j1 - j0 == 1) mma_commit_p(&bars->q_empty, leader);
-      for (int j = j0; j < j1; ++j, ++kv, ++g) {
-        const int st = kv % C::NSTAGE, st2 = (kv + 1) % C::NSTAGE;
-        const bool more = j + 1 < j1;
+      for (int j = j0; j < j1; ++j, ++kv) {
+        const int st = kv % C::NSTAGE;
+        if (!(ok = pv_complete(kv - 1))) break;
+        if (j + 1 < j1) {
+          const int i = kv + 1;
+          if (!(ok = warp_wait(&bars->k_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns, abort_flag, 324))) break;
+          tc_fence_after();
+          issue_S(i, i);
+          if (j + 2 == j1) mma_commit_p(&bars->q_empty, leader);  // the item's last scores
+        }
         if (!(ok = warp_wait(&bars->v_full[st], (kv / C::NSTAGE) & 1, p.wait_ns, abort_flag, 322))) break;
         if ((P & 15) != 0 && (P - 1) / C::BN == j) {  // V rows of the last block's unused slots: zero
           uint8_t* sv = smem + C::OFF_V + st * C::KV_TILE;
@@ -222,28 +255,14 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!(ok = warp_wait(&bars->p_full[0], g & 1, p.wait_ns, abort_flag, 323))) break;
-        tc_fence_after();
-        issue_PV(0, st, j == j0);
-        if (more) {
-          if (!(ok = warp_wait(&bars->k_full[st2], ((kv + 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag, 324))) break;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (!(ok = warp_wait(&bars->p_full[t][kv & 1], (kv >> 1) & 1, p.wait_ns, abort_flag, 323 + 2 * t))) break;
           tc_fence_after();
-          issue_S(0, st2);
-          mma_commit_p(&bars->s_full[0], leader);
-        } else {
-          mma_commit_p(&bars->o_final[0], leader);
+          issue_PV(t, st, kv, j == j0);
+          if (j + 1 == j1) mma_commit_p(&bars->o_final[t], leader);
         }
-        if (!(ok = warp_wait(&bars->p_full[1], g & 1, p.wait_ns, abort_flag, 325))) break;
-        tc_fence_after();
-        issue_PV(1, st, j == j0);
-        mma_commit_p(&bars->kv_empty[st], leader);
-        if (more) {
-          issue_S(1, st2);
-          mma_commit_p(&bars->s_full[1], leader);
-          if (j + 2 == j1) mma_commit_p(&bars->q_empty, leader);  // that was the item's last S
-        } else {
-          mma_commit_p(&bars->o_final[1], leader);
-        }
+        if (!ok) break;
+        mma_commit_p(&bars->v_empty[st], leader);
       }
     }
     if (!ok) {  // likewise the MMAs, before TMEM is given back
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
     const int t = (warp - 2) >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;  // row of the tile == TMEM lane
     const uint32_t lane_off = uint32_t(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::COL_S + t * C::BN, tO = tmem + lane_off + C::COL_O + t * D;
+    const uint32_t tO = tmem + lane_off + C::COL_O + t * D;
     const float sl2 = p.scale_log2;
     int g = 0, local = 0;
     bool ok = true;
@@ -267,7 +286,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
       const bool idle = __all_sync(0xffffffffu, r >= p.G * p.RT || req >= p.R);
       float m = -INFINITY, l = 0.f;
       for (int j = j0; j < j1; ++j, ++g) {
-        if (!(ok = warp_wait(&bars->s_full[t], g & 1, p.wait_ns, abort_flag, 330 + t))) break;
+        const uint32_t tS = tmem + lane_off + (2 * (g & 1) + t) * C::BN;
+        if (!(ok = warp_wait(&bars->s_full[t][g & 1], (g >> 1) & 1, p.wait_ns, abort_flag, 330 + t))) break;
         if (!idle) {
           tc_fence_after();
           uint32_t sr[C::BN];
@@ -313,6 +333,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
           const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
           l = l * alpha + (rsa.x + rsa.y);
           if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // u must hold the tile before this one, and no later one can have been added yet (this
+            // step's scores were issued after P V of two steps before, whose phase is over)
+            if (!(ok = warp_wait(&bars->pv_done[t], (g - 1) & 1, p.wait_ns, abort_flag, 332 + t))) break;
+            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -328,7 +352,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+        if (lane == 0) mbar_arrive(&bars->p_full[t][g & 1]);
       }
       if (ok) ok = warp_wait(&bars->o_final[t], local & 1, p.wait_ns, abort_flag, 340 + t);
       if (!ok) break;

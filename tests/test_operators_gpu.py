@@ -309,8 +309,9 @@ def test_decode_shared(d, Hq, Hkv, prefix, lens):
     V, _ = ops.decode_shared(q, kc, vc.abs(), ptable, prefix, table, ctx, 16, d**-0.5)
     near(o, O, slack + 2.0**-8 * V, "o")
     near(lse, L, delta + 2.0**-20 * np.abs(np.where(np.isinf(L), 0, L)), "lse")
-    again, _ = fa.paged_decode_shared(*dev, with_lse=False)
-    assert torch.equal(o, again)
+    for _ in range(8):  # (a race between the roles of the prefix kernel once showed as runs that differ)
+        again, _ = fa.paged_decode_shared(*dev, with_lse=False)
+        assert torch.equal(o, again)
 
 
 @pytest.mark.parametrize("d", [64, 128])
