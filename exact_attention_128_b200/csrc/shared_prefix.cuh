@@ -11,15 +11,15 @@
 // nt = ceil(P / BN) key tiles, and CTA c of C takes tiles [c W / C, (c + 1) W / C) of all W =
 // items * nt: every CTA does the same work, whatever the batch and the prefix (P is read on the
 // device), and an item's tiles fall to a few consecutive CTAs, one partial result each.
-//   warp 0     producer (whole warp): Q by TMA per item; lane i < BN / 16 looks block i of a K/V
-//              tile up in the prefix table and issues its 16-row boxes.
+//   warp 0     producer of Q (by TMA, per item) and K: lane i < BN / 16 looks block i of a key tile
+//              up in the prefix table and issues its 16-row boxes; warp V_WARP the same for V.
 //   warp 1     MMA issuer: S_t = Q_t K^T into TMEM, then u_t += P_t V with P_t read from TMEM.
 //   warps 2-9  softmax of row tiles 0 and 1, one thread per row.
 // Scores are double-buffered in TMEM and issued one key tile ahead, so a softmax warp goes from
 // one tile to the next without waiting for its own P V (with one buffer, the chain S, softmax,
 // P V of a 64-key tile took 3290 cycles a step of two row tiles; MMAs alone take about 1100).
 // Only the rare step whose maximum rises waits for the P V before it, to rescale u.
-// BN = 64 and two K/V stages keep the CTA at 150 KB of shared memory and 320 threads of at most
+// BN = 64 and two K/V stages keep the CTA at 150 KB of shared memory and 352 threads of at most
 // 104 registers, so that a CTA of the requests' own (memory-bound) part runs on the SM beside it.
 // P is rounded to bf16 for P V: with many rows the tensor core is what bounds this part, and the
 // second product that would carry P's rest would cost it half as much again.
@@ -38,7 +38,7 @@ struct PrefixCfg {
   static constexpr int OFF_Q = 0, OFF_K = 2 * Q_TILE, OFF_V = OFF_K + NSTAGE * KV_TILE;
   static constexpr int OFF_STG = OFF_V + NSTAGE * KV_TILE, OFF_BAR = OFF_STG + 8 * STG_WARP;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;  // + barriers, alignment of the base
-  static constexpr int THREADS = 320;
+  static constexpr int V_WARP = 10, THREADS = 352;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_O = 4 * BN;  // S of row tile t, buffer b at (2 b + t) * BN; u_t at COL_O + t * D
   static_assert(4 * BN + 2 * D <= 512, "TMEM");
@@ -65,8 +65,10 @@ struct PrefixBars {
 };
 static_assert(sizeof(PrefixBars) <= 256, "barrier area");
 
+// (launched with fewer threads than its bound: 608 threads leave 104 registers to each, so that the
+// register file holds a CTA of the requests' own part too)
 template <int D>
-__global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
+__global__ void __launch_bounds__(608)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p) {
   using C = PrefixCfg<D>;
@@ -119,38 +121,42 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
   const long long x0 = any ? deal.begin(blockIdx.x) : 0, x1 = any ? deal.begin(blockIdx.x + 1) : 0;
   const int nblk = (P + 15) / 16;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == C::V_WARP) {
+    // K (and Q) and V have a producer each: neither waits for the other's stage, so a load is
+    // issued two steps before its tile is due.
     constexpr int NB = C::BN / 16;
+    const bool is_v = warp != 0;
+    const CUtensorMap* map = is_v ? &tmV : &tmK;
+    uint64_t* full = is_v ? bars->v_full : bars->k_full;
+    uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+    uint8_t* ring = smem + (is_v ? C::OFF_V : C::OFF_K);
     if (lane == 0) {
-      prefetch_tmap(&tmQ);
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
+      prefetch_tmap(map);
+      if (!is_v) prefetch_tmap(&tmQ);
     }
-    int kv = 0, kv_k = 0, local = 0;  // V and K tiles issued
+    int kv = 0, local = 0;  // tiles issued, items begun
     bool ok = true;
     for (long long x = x0; x < x1 && ok; ++local) {
       const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
       const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
       x += j1 - j0;
       const int hk = it / p.pairs, pair = it - hk * p.pairs;
-      if (local > 0 && !(ok = warp_wait(&bars->q_empty, (local - 1) & 1, p.wait_ns, abort_flag, 311))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full, uint32_t(2 * C::KB * 128 * p.G * p.RT));
-        for (int t = 0; t < 2; ++t)
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_3d(smem + C::OFF_Q + t * C::Q_TILE + kb * C::BM * 128, &tmQ, &bars->q_full, kb * 64, hk * p.G,
-                        (2 * pair + t) * p.RT);
-      }
       int ph = (lane < NB && j0 * NB + lane < nblk) ? __ldg(p.pbt + j0 * NB + lane) : 0;
+      if (!is_v) {
+        if (local > 0 && !(ok = warp_wait(&bars->q_empty, (local - 1) & 1, p.wait_ns, abort_flag, 311))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, uint32_t(2 * C::KB * 128 * p.G * p.RT));
+          for (int t = 0; t < 2; ++t)
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_3d(smem + C::OFF_Q + t * C::Q_TILE + kb * C::BM * 128, &tmQ, &bars->q_full, kb * 64, hk * p.G,
+                          (2 * pair + t) * p.RT);
+        }
+      }
       for (int j = j0; j < j1; ++j, ++kv) {
         const int st = kv % C::NSTAGE, round = kv / C::NSTAGE;
         const int lb = j * NB + lane;
         const int ph_next = (lane < NB && j + 1 < j1 && lb + NB < nblk) ? __ldg(p.pbt + lb + NB) : 0;
-        if (round > 0 && !(ok = warp_wait(&bars->k_empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 310))) break;
-        uint8_t* sk = smem + C::OFF_K + st * C::KV_TILE;
-        uint8_t* sv = smem + C::OFF_V + st * C::KV_TILE;
         const int nload = min(NB, nblk - j * NB);  // >= 1
-        const uint32_t bytes = uint32_t(nload) * 16 * 128 * C::KB;
         int crow = 0;
         if (lane < nload) {
           int pb = ph;
@@ -160,33 +166,27 @@ __global__ void __launch_bounds__(PrefixCfg<D>::THREADS, 2)
           }
           crow = (pb * p.Hkv + hk) * 16;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], bytes);
-        __syncwarp();
-        if (lane < nload)
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_2d(smem_u32(sk + kb * C::BN * 128 + lane * 16 * 128), &tmK, &bars->k_full[st], kb * 64, crow);
-        ++kv_k;
-        if (round > 0 && !(ok = warp_wait(&bars->v_empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 312))) break;
-        if (nload < NB) {  // V rows of blocks past the prefix: zero (their P is 0; 0 * NaN would not be)
+        ph = ph_next;
+        if (round > 0 && !(ok = warp_wait(&empty[st], (round - 1) & 1, p.wait_ns, abort_flag, 310 + 2 * is_v))) break;
+        uint8_t* tile = ring + st * C::KV_TILE;
+        if (is_v && nload < NB) {  // V rows of blocks past the prefix: zero (their P is 0; 0 * NaN would not be)
           for (int kb = 0; kb < C::KB; ++kb)
             for (int i = nload * 128 + lane; i < C::BN * 8; i += 32)
-              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(tile + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
+          __syncwarp();
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[st], bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(nload) * 16 * 128 * C::KB);
         __syncwarp();
         if (lane < nload)
           for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_2d(smem_u32(sv + kb * C::BN * 128 + lane * 16 * 128), &tmV, &bars->v_full[st], kb * 64, crow);
-        ph = ph_next;
+            tma_load_2d(smem_u32(tile + kb * C::BN * 128 + lane * 16 * 128), map, &full[st], kb * 64, crow);
       }
     }
     if (!ok && lane == 0) {  // a wait ran out: let the loads in flight land before the CTA ends
-      for (int i = max(0, kv_k - C::NSTAGE); i < kv_k; ++i)
-        mbar_wait_bounded(&bars->k_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
       for (int i = max(0, kv - C::NSTAGE); i < kv; ++i)
-        mbar_wait_bounded(&bars->v_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
-      if (local > 0) mbar_wait_bounded(&bars->q_full, (local - 1) & 1, p.wait_ns);
+        mbar_wait_bounded(&full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns);
+      if (!is_v && local > 0) mbar_wait_bounded(&bars->q_full, (local - 1) & 1, p.wait_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
