@@ -8,9 +8,18 @@
 // A token's age is not its slot then; slot_pos carries each slot's sequence position (-1: not
 // moved since it was appended, so its position is seq_len - n + slot).
 //
-// Selection: each token's key is its weight as an order-preserving 32-bit integer, all ones where
-// it is protected; the keep-th largest key is found digit by digit from histograms.  One CTA per
-// (r, h) selects and writes the lists of moves, a second kernel moves the rows.
+// One CTA per (r, h).  Each token's key is its weight as an order-preserving 32-bit integer, all
+// ones where it is protected, and is kept in shared memory (read again from the inputs past
+// MAX_KEYS tokens).  The keep-th largest key is found in three digits of 9, 11 and 12 bits, from a
+// histogram each.  The first digit is a weight's exponent, of which few differ: its histogram has
+// 16 copies, one for every other lane, so that the lanes of a warp seldom add to one address (with
+// one copy of an 11-bit digit the selection of 8192 tokens took 32 us, most of it there).  Which tokens are above it, and which equal it, become bit masks of 32 tokens;
+// prefix sums of their population counts give every freed slot and every moving token its number.
+// The CTA then moves the rows itself, or, where there are too few CTAs for the moves to fill the
+// device, a second kernel does.
+//
+// What bounds it: long prompts, the rows that move; steady eviction of few tokens, the latency of
+// the selection's passes over shared memory.
 #pragma once
 #include "common.cuh"
 
@@ -18,20 +27,26 @@ namespace fa {
 namespace evict {
 constexpr int THREADS = 512;
 constexpr int BS = 16;
+constexpr int COPIES = 16;       // of the first digit's histogram
+constexpr int BINS = 512 * COPIES;
+constexpr int MAX_KEYS = 40960;  // tokens whose keys (and masks) fit in shared memory
 }  // namespace evict
 
 struct EvictParams {
   const int *bt, *ctx, *seq;
-  const float* weights;   // [R, Hkv, M], M = max_blocks * 16
-  const int* slot_pos;    // [R, Hkv, M]
+  const float* weights;  // [R, Hkv, M], M = max_blocks * 16
+  const int* slot_pos;   // [R, Hkv, M]
   float* weights_out;
   int* slot_pos_out;
-  int* new_ctx;           // [R]
-  int* moves;             // [R * Hkv][2 * cap]: destinations, then sources
-  int* n_moves;           // [R * Hkv]
+  int* new_ctx;    // [R]
+  int* moves;      // [R * Hkv][2 * cap]: destinations, then sources, as cache rows (block * Hkv + h) * 16 + slot
+  int* n_moves;    // [R * Hkv]
+  uint32_t* masks; // [R * Hkv][2][ceil(M / 32)], past MAX_KEYS only
   uint4 *kc, *vc;
   int R, Hkv, max_blocks, num_blocks, keep, recent, cap;
-  int row16;              // 16-byte pieces of a cache row
+  int row16;       // 16-byte pieces of a cache row
+  bool in_smem;    // keys, masks and lists in shared memory
+  bool fused;      // this kernel moves the rows (in_smem only)
 };
 
 // Larger weight, larger key; -0 as +0; NaN below everything.
@@ -41,160 +56,258 @@ __device__ __forceinline__ uint32_t evict_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the CTA of v (two 16-bit halves), and the total.
-__device__ __forceinline__ uint32_t evict_scan(uint32_t v, uint32_t* s_warp, uint32_t& total) {
+// Exclusive prefix sum of v over the CTA, and the total.
+__device__ __forceinline__ int evict_scan(int v, int* s_warp, int& total) {
   const int lane = lane_id(), warp = warp_id();
-  uint32_t x = v;
+  int x = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
   __syncthreads();  // the last call's readers are done
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  int before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < evict::THREADS / 32; ++w) {
-    const uint32_t t = s_warp[w];
-    before += w < warp ? t : 0u;
+    const int t = s_warp[w];
+    before += w < warp ? t : 0;
     all += t;
   }
   total = all;
   return before + x - v;
 }
 
+// Copy `moves` key and value rows: a group of lanes a row, thread t of `threads`.  U rows are read
+// before the first is written, so a thread has 2 U pieces of 16 bytes in flight.
+__device__ __forceinline__ void evict_move_rows(const EvictParams& p, const int* dst, const int* src, int moves, int t,
+                                                int threads) {
+  const int lanes = p.row16 <= 8 ? 8 : p.row16 <= 16 ? 16 : 32;  // 96 columns: 12 of 16 work
+  const int e = t & (lanes - 1), step = threads / lanes;
+  if (e >= p.row16) return;
+  constexpr int U = 2;
+  for (int64_t i = t / lanes; i < moves; i += U * step) {
+    uint4 k[U], v[U];
+    int to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = i + u * step;
+      to[u] = -1;
+      if (at < moves) {
+        const int a = src[at];
+        to[u] = a < 0 ? -1 : dst[at];  // (a block id out of range was flagged)
+        if (to[u] >= 0) {
+          k[u] = p.kc[size_t(a) * p.row16 + e];
+          v[u] = p.vc[size_t(a) * p.row16 + e];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (to[u] >= 0) {
+        p.kc[size_t(to[u]) * p.row16 + e] = k[u];
+        p.vc[size_t(to[u]) * p.row16 + e] = v[u];
+      }
+  }
+}
+
 __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const __grid_constant__ EvictParams p) {
   using namespace evict;
-  __shared__ int s_hist[256];
-  __shared__ uint32_t s_warp[THREADS / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  extern __shared__ uint32_t evict_smem[];
+  __shared__ int s_hist[BINS];
+  __shared__ int s_warp[THREADS / 32];
+  __shared__ int s_found[2];  // the digit's bin, and how many of its tokens are still needed
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+  const int r = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = lane_id();
   const size_t rh = size_t(r) * p.Hkv + h;
   const int M = p.max_blocks * BS;
   const float* w = p.weights + rh * M;
   const int* sp = p.slot_pos + rh * M;
   float* wo = p.weights_out + rh * M;
   int* so = p.slot_pos_out + rh * M;
-  int n = p.ctx[r];
-  const int seq = p.seq[r];
-  if (n < 0 || n > M || seq < n) {
+  const int* bt = p.bt + size_t(r) * p.max_blocks;
+  const int n = p.ctx[r], seq = p.seq[r];
+  const bool bad = n < 0 || n > M || seq < n;
+  if (bad || n <= p.keep) {  // out of range: left as it is; nothing to evict: the positions are written down
     if (tid == 0) {
-      set_status(FA_ERR_INVALID_ARG, 400);
+      if (bad) set_status(FA_ERR_INVALID_ARG, 400);
       p.n_moves[rh] = 0;
       if (h == 0) p.new_ctx[r] = n;
     }
     for (int s = tid; s < M; s += THREADS) {
-      wo[s] = w[s];
-      so[s] = sp[s];
+      const int pos = sp[s];
+      const float v = w[s];
+      wo[s] = bad || s < n ? v : 0.f;
+      so[s] = bad ? pos : s >= n ? -1 : pos >= 0 ? pos : seq - n + s;
     }
     return;
   }
-  if (tid == 0 && h == 0) p.new_ctx[r] = min(n, p.keep);
-  auto pos_of = [&](int s) {
-    const int v = sp[s];
-    return v >= 0 ? v : seq - n + s;
-  };
-  auto key_of = [&](int s) { return pos_of(s) >= seq - p.recent ? 0xffffffffu : evict_key(w[s]); };
-
-  uint32_t thr = 0;  // the keep-th largest key; `ties` of the tokens that have it are kept
-  int ties = n;
-  if (n > p.keep) {
-    if (tid == 0) {
-      s_prefix = 0;
-      s_need = p.keep;
+  if (tid == 0 && h == 0) p.new_ctx[r] = p.keep;
+  auto pos_of = [&](int s, int v) { return v >= 0 ? v : seq - n + s; };
+  const int newest = seq - p.recent;
+  auto key_from = [&](int s, float wt, int v) { return pos_of(s, v) >= newest ? 0xffffffffu : evict_key(wt); };
+  const int words = (n + 31) / 32, MW = (M + 31) / 32;
+  uint32_t* s_key = evict_smem;                                           // [n]
+  uint32_t* above = p.in_smem ? evict_smem + M : p.masks + rh * 2 * MW;  // [words]: key above the threshold, kept
+  uint32_t* equal = above + MW;                                           // [words]: key at it; then the words' numbers
+  const float4* w4 = reinterpret_cast<const float4*>(w);
+  const int4* sp4 = reinterpret_cast<const int4*>(sp);
+  for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
+  if (p.in_smem) {
+#pragma unroll 2
+    for (int i = tid; 4 * i < n; i += THREADS) {  // (keys past n are not used)
+      const float4 a = __ldg(w4 + i);
+      const int4 v = __ldg(sp4 + i);
+      reinterpret_cast<uint4*>(s_key)[i] = make_uint4(key_from(4 * i, a.x, v.x), key_from(4 * i + 1, a.y, v.y),
+                                                      key_from(4 * i + 2, a.z, v.z), key_from(4 * i + 3, a.w, v.w));
     }
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += THREADS) s_hist[i] = 0;
-      __syncthreads();
-      const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int s = tid; s < n; s += THREADS) {
-        const uint32_t k = key_of(s);
-        if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int need = s_need, b = 255;
-        for (; b > 0 && s_hist[b] < need; --b) need -= s_hist[b];
-        s_need = need;
-        s_prefix = prefix | (uint32_t(b) << shift);
-      }
-      __syncthreads();
-    }
-    thr = s_prefix;
-    ties = s_need;
-  }
-
-  // slots in order: which are kept, the freed ones below `keep`, the kept ones past it
-  const int lim = min(n, p.keep);
-  int* dst = p.moves + rh * 2 * p.cap;
-  int* src = dst + p.cap;
-  int eq_before = 0, holes = 0, movers = 0;
-  for (int base = 0; base < n; base += THREADS) {
-    const int s = base + tid;
-    uint32_t key = 0;
-    int pos = -1;
-    float wt = 0.f;
-    if (s < n) {
-      pos = pos_of(s);
-      wt = w[s];
-      key = pos >= seq - p.recent ? 0xffffffffu : evict_key(wt);
-    }
-    const bool eq = s < n && key == thr;
-    uint32_t total;
-    const uint32_t rank = evict_scan(eq ? 1u : 0u, s_warp, total);
-    const bool kept = s < n && (n <= p.keep || key > thr || (eq && int(rank) + eq_before < ties));
-    eq_before += total;
-    const bool hole = s < lim && !kept, mover = kept && s >= p.keep;
-    const uint32_t at = evict_scan((hole ? 1u : 0u) | (mover ? 0x10000u : 0u), s_warp, total);
-    if (hole) dst[holes + (at & 0xffff)] = s;
-    if (mover) src[movers + (at >> 16)] = s;
-    holes += total & 0xffff;
-    movers += total >> 16;
-    if (s < n) {
-      const bool stays = kept && s < p.keep;
-      wo[s] = stays ? wt : 0.f;
-      so[s] = stays ? pos : -1;
-    }
-  }
-  for (int s = n + tid; s < M; s += THREADS) {
-    wo[s] = 0.f;
-    so[s] = -1;
   }
   __syncthreads();
-  if (tid == 0) p.n_moves[rh] = movers;  // == holes
-  for (int i = tid; i < movers; i += THREADS) {
-    wo[dst[i]] = w[src[i]];
-    so[dst[i]] = pos_of(src[i]);
+  auto key_of = [&](int s) { return p.in_smem ? s_key[s] : key_from(s, __ldg(w + s), __ldg(sp + s)); };
+
+  // the keep-th largest key, digit by digit; `need` of the tokens that have it are kept
+  uint32_t thr = 0;
+  int need = p.keep;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 23 : pass == 1 ? 12 : 0;
+    const int bins = pass == 0 ? 512 : pass == 1 ? 2048 : 4096;
+    const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 23 : 12);
+    for (int s = tid; s < n; s += THREADS) {
+      const uint32_t k = key_of(s);
+      const int bin = (k >> shift) & (bins - 1);
+      if ((k & mask) == thr) atomicAdd(&s_hist[pass == 0 ? bin * COPIES + (lane & (COPIES - 1)) : bin], 1);
+    }
+    __syncthreads();
+    // a few bins a thread, the highest first
+    const int per = bins / THREADS, top = bins - 1 - per * tid;
+    int c[8], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+      c[i] = 0;
+      if (pass == 0) {
+#pragma unroll
+        for (int j = 0; j < COPIES; ++j) c[i] += s_hist[(top - i) * COPIES + ((j + lane) & (COPIES - 1))];
+      } else {
+        c[i] = s_hist[top - i];
+      }
+      sum += c[i];
+    }
+    int before = evict_scan(sum, s_warp, total);
+    if (before < need && need <= before + sum) {
+#pragma unroll
+      for (int i = 0; i < per; ++i) {
+        if (before < need && need <= before + c[i]) {
+          s_found[0] = top - i;
+          s_found[1] = need - before;
+        }
+        before += c[i];
+      }
+    }
+    if (pass < 2)
+      for (int i = tid; i < 4096; i += THREADS) s_hist[i] = 0;  // (every thread has read its bins: evict_scan)
+    __syncthreads();
+    thr |= uint32_t(s_found[0]) << shift;
+    need = s_found[1];
   }
+
+#pragma unroll 4
+  for (int s = tid; s - lane < n; s += THREADS) {  // (whole warps)
+    const uint32_t k = s < n ? key_of(s) : 0u;
+    const uint32_t a = __ballot_sync(0xffffffffu, s < n && k > thr), e = __ballot_sync(0xffffffffu, s < n && k == thr);
+    if (lane == 0) {
+      above[s >> 5] = a;
+      equal[s >> 5] = e;
+    }
+  }
+  __syncthreads();
+  // kept = above, and the first `need` at the threshold; then each word's first number among the
+  // freed slots (below keep) and the moving tokens (past it)
+  int eq_done = 0, hole_done = 0, mover_done = 0;
+  for (int b = 0; b < words; b += THREADS) {
+    const int i = b + tid;
+    const uint32_t a = i < words ? above[i] : 0u;
+    uint32_t e = i < words ? equal[i] : 0u;
+    int total;
+    const int skip = need - (eq_done + evict_scan(__popc(e), s_warp, total));  // of this word's, so many are kept
+    eq_done += total;
+    int drop = __popc(e) - max(0, skip);
+    for (; drop > 0; --drop) e &= ~(0x80000000u >> __clz(e));
+    const uint32_t kept = a | e;
+    // bits of slots below keep, and of slots below n
+    const int lo = p.keep - 32 * i, hi = n - 32 * i;
+    const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? 0xffffffffu : (1u << lo) - 1;
+    const uint32_t live = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1;
+    const int holes = __popc(~kept & below & live), movers = __popc(kept & ~below);
+    const int hole = evict_scan(holes, s_warp, total) + hole_done;
+    hole_done += total;
+    const int mover = evict_scan(movers, s_warp, total) + mover_done;
+    mover_done += total;
+    if (i < words) {
+      above[i] = kept;
+      equal[i] = uint32_t(lo > 0 ? hole : mover);  // (in the one word that may hold both, movers start at 0)
+    }
+  }
+  __syncthreads();
+  const int moves = mover_done;  // == hole_done
+  // the lists take the keys' place once nothing reads a key (moves <= n / 2)
+  int* dst = p.in_smem && p.fused ? reinterpret_cast<int*>(s_key) : p.moves + rh * 2 * p.cap;
+  int* src = dst + (p.in_smem && p.fused ? M / 2 : p.cap);
+#pragma unroll 2
+  for (int i = tid; 4 * i < M; i += THREADS) {
+    float4 wt = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 pos = make_int4(-1, -1, -1, -1);
+    if (4 * i < n) {
+      const float4 a = __ldg(w4 + i);
+      const int4 v = __ldg(sp4 + i);
+      const uint32_t kept = above[i >> 3], number = equal[i >> 3];
+      const int first = (4 * i) & ~31, lo = p.keep - first;
+      // movers of this word: its kept tokens past keep
+      const uint32_t past = kept & (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = 4 * i + j;
+        const uint32_t bit = 1u << (s & 31);
+        if (s >= n) continue;
+        if (s >= p.keep) {
+          if (kept & bit) src[(lo > 0 ? 0 : int(number)) + __popc(past & (bit - 1))] = s;
+        } else if (kept & bit) {
+          (j == 0 ? wt.x : j == 1 ? wt.y : j == 2 ? wt.z : wt.w) = j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w;
+          (j == 0 ? pos.x : j == 1 ? pos.y : j == 2 ? pos.z : pos.w) =
+              pos_of(s, j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
+        } else {
+          dst[int(number) + __popc(~kept & (bit - 1))] = s;
+        }
+      }
+    }
+    reinterpret_cast<float4*>(wo)[i] = wt;
+    reinterpret_cast<int4*>(so)[i] = pos;
+  }
+  __syncthreads();
+  if (tid == 0) p.n_moves[rh] = moves;
+#pragma unroll 2
+  for (int i = tid; i < moves; i += THREADS) {
+    const int a = src[i], b = dst[i];
+    wo[b] = __ldg(w + a);
+    so[b] = pos_of(a, __ldg(sp + a));
+    // from slots to cache rows
+    const int pa = __ldg(bt + a / BS), pb = __ldg(bt + b / BS);
+    const bool ok = pa >= 0 && pa < p.num_blocks && pb >= 0 && pb < p.num_blocks;
+    if (!ok) set_status(FA_ERR_INVALID_ARG, 401);
+    src[i] = ok ? (pa * p.Hkv + h) * BS + a % BS : -1;
+    dst[i] = ok ? (pb * p.Hkv + h) * BS + b % BS : -1;
+  }
+  if (!p.fused) return;
+  __syncthreads();
+  evict_move_rows(p, dst, src, moves, tid, THREADS);
 }
 
-// 32 threads per move at 128 columns: 16 for the key's 16-byte pieces, 16 for the value's.
 __global__ void __launch_bounds__(256) fa_evict_move_kernel(const __grid_constant__ EvictParams p) {
-  using namespace evict;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r = blockIdx.z, h = blockIdx.y;
-  const size_t rh = size_t(r) * p.Hkv + h;
-  const int moves = p.n_moves[rh];
+  const size_t rh = size_t(blockIdx.z) * p.Hkv + blockIdx.y;
   const int* dst = p.moves + rh * 2 * p.cap;
-  const int* src = dst + p.cap;
-  const int* bt = p.bt + size_t(r) * p.max_blocks;
-  const int per = 2 * p.row16;
-  const int64_t all = int64_t(moves) * per;
-  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < all; t += int64_t(gridDim.x) * 256) {
-    const int i = int(t / per), piece = int(t % per);
-    const int a = src[i], b = dst[i];
-    const int pa = bt[a / BS], pb = bt[b / BS];
-    if (pa < 0 || pa >= p.num_blocks || pb < 0 || pb >= p.num_blocks) {
-      set_status(FA_ERR_INVALID_ARG, 401);
-      continue;
-    }
-    uint4* c = piece < p.row16 ? p.kc : p.vc;
-    const int e = piece < p.row16 ? piece : piece - p.row16;
-    c[((size_t(pb) * p.Hkv + h) * BS + b % BS) * p.row16 + e] = c[((size_t(pa) * p.Hkv + h) * BS + a % BS) * p.row16 + e];
-  }
+  evict_move_rows(p, dst, dst + p.cap, p.n_moves[rh], blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 }  // namespace fa

@@ -401,6 +401,9 @@ def evict_case(lens, Hkv, d, maxb, keep, seed, kind="random"):
         ((640, 129), 2, 64, 77, 20, "odd"),
         ((5000,), 1, 64, 1024, 128, "random"),
         ((4096, 4097), 2, 64, 4096, 512, "ties"),
+        ((2100, 1000, 2048) * 13, 2, 64, 1000, 100, "random"),  # enough CTAs to move their own rows
+        ((3000, 2999), 1, 128, 1500, 0, "ties"),  # too few: a second kernel moves them
+        ((50000,), 1, 64, 20000, 5000, "ties"),  # keys past shared memory
     ],
 )
 def test_evict(lens, Hkv, d, keep, recent, kind):
