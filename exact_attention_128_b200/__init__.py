@@ -535,7 +535,7 @@ def paged_decode_shared_workspace_size(R, Hq, Hkv, d, max_prefix_blocks, max_blo
 
 def _decode_outputs(q, shape, device, with_lse, out):
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q)
     op = _expect("out", out, shape, torch.bfloat16, device)
     if not with_lse:
         return out, None, op, 0

@@ -53,7 +53,8 @@ struct PartParams {
   const int* plen;         // prefix tokens [1] (shared only)
   int R, Hq, Hkv, max_blocks, prefix_blocks, num_blocks;
   int parts;               // partial results per row: prefix pieces, then own pieces
-  int prefix_parts;
+  int prefix_parts, own_parts;
+  int n_prefix;            // CTAs that work on prefix pieces
   int chunk, prefix_chunk;  // blocks of a piece
   // the prefix part by the tensor-core kernel (shared_prefix.cuh): its results, else null
   const float *pre_o, *pre_lse;
@@ -71,7 +72,8 @@ __device__ __forceinline__ int part_len(const int* len, int i, int max_blocks, i
   return -1;
 }
 
-template <int D, bool PREFIX, bool SCORED>
+// CTAs [0, n_prefix) take the prefix's pieces, the others the requests' own.
+template <int D, bool SCORED>
 __global__ void __launch_bounds__(part::WARPS * 32)
     fa_decode_part_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ PartParams p) {
@@ -80,33 +82,32 @@ __global__ void __launch_bounds__(part::WARPS * 32)
   constexpr int KS = D / 16, NT = D / 8, KB = D / 64;
   extern __shared__ uint8_t dsmem_raw[];
   uint8_t* dsmem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~uintptr_t(1023));
-  const int s = blockIdx.x, g = blockIdx.y, z = blockIdx.z;  // piece, kv head, request or row tile
-  const int G = p.Hq / p.Hkv;
+  const bool prefix = int(blockIdx.x) < p.n_prefix;
+  const int parts = prefix ? p.prefix_parts : p.own_parts, at = prefix ? blockIdx.x : blockIdx.x - p.n_prefix;
+  const int zg = at / parts, s = at - zg * parts;                // piece
+  const int z = zg / p.Hkv, g = zg - z * p.Hkv, G = p.Hq / p.Hkv;  // request or row tile, kv head
   // late_wait: the prefix kernel let this grid start once it had waited for everything before it.
   // Its own results are read by the grid after this one, which waits for this grid alone: so one
   // CTA, the last to be started, holds this grid open until the prefix kernel is done.
-  const bool hold = p.late_wait && s == int(gridDim.x) - 1 && g == int(gridDim.y) - 1 && z == int(gridDim.z) - 1;
+  const bool hold = p.late_wait && blockIdx.x == gridDim.x - 1;
   auto finish = [&] {
     if (hold) asm volatile("griddepcontrol.wait;" ::: "memory");
   };
   if (!p.late_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int n = PREFIX ? part_len(p.plen, 0, p.prefix_blocks, 302) : part_len(p.ctx, z, p.max_blocks, 300);
-  const int chunk = PREFIX ? p.prefix_chunk : p.chunk;
+  const int n = prefix ? part_len(p.plen, 0, p.prefix_blocks, 302) : part_len(p.ctx, z, p.max_blocks, 300);
+  const int chunk = prefix ? p.prefix_chunk : p.chunk;
   const int nblk = (n + BS - 1) / BS;
   const int b0 = s * chunk;
   if (n <= 0 || b0 >= nblk) return finish();
   const int b1 = min(nblk, b0 + chunk);
-  const int* bt = PREFIX ? p.pbt : p.bt + size_t(z) * p.max_blocks;
-  const int rows = PREFIX ? min(ROWS, p.R * G - z * ROWS) : G;
+  const int* bt = prefix ? p.pbt : p.bt + size_t(z) * p.max_blocks;
+  const int rows = prefix ? min(ROWS, p.R * G - z * ROWS) : G;
   // (request, head) of row i, as one index into [R * Hq]
   auto row_of = [&](int i) {
-    if constexpr (PREFIX) {
-      const int j = z * ROWS + i;
-      return (j / G) * p.Hq + g * G + j % G;
-    } else {
-      return z * p.Hq + g * G + i;
-    }
+    if (!prefix) return z * p.Hq + g * G + i;
+    const int j = z * ROWS + i;
+    return (j / G) * p.Hq + g * G + j % G;
   };
 
   const int warp = warp_id(), lane = lane_id();
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(part::WARPS * 32)
   l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
   __syncthreads();  // all warps are done with their stages: reuse shared memory
-  const int part = PREFIX ? s : p.prefix_parts + s;
+  const int part = prefix ? s : p.prefix_parts + s;
   if (abort_flag) {  // NaN, so that nothing merged from this piece looks valid
     for (int i = threadIdx.x; i < rows; i += WARPS * 32) p.part_lse[size_t(row_of(i)) * p.parts + part] = NAN;
     return finish();

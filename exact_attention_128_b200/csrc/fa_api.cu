@@ -2,6 +2,7 @@
 // encoding and kernel launches.  Everything that computes runs in the kernels;
 // this file only checks arguments and launches them on the caller's stream.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <mutex>

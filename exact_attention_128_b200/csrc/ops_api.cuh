@@ -20,6 +20,34 @@
 
 namespace {
 
+// A kernel whose launches need attributes (dynamic shared memory past 48 KB, the SM's memory as
+// shared memory): they are set at its first launch on each device, and again should a launch fail
+// (a reset device has forgotten them).
+class Prepared {
+ public:
+  template <typename... KArgs, typename... Args>
+  cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, int smem, cudaStream_t st, const Args&... args) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    std::atomic<int>& have = smem_[dev & 63];
+    if (have.load(std::memory_order_relaxed) >= smem) {
+      if (launch_pdl(kernel, grid, block, smem, st, args...) == cudaSuccess) return cudaSuccess;
+      cudaGetLastError();
+    }
+    if (cudaError_t e = set_smem(kernel, smem)) return e;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared))
+      return e;
+    have.store(smem, std::memory_order_relaxed);
+    return launch_pdl(kernel, grid, block, smem, st, args...);
+  }
+
+ private:
+  std::atomic<int> smem_[64] = {};
+};
+
+constexpr int kSms = 148;  // SMs that work is divided for
+
 // Rotation arguments that every rotary entry point shares: sizes, then one of `out` launches.
 fa_status rope_check(const int* positions, const double* inv_freq, int B, int Hq, int Hkv, int N, int d, int rotary_dim,
                      const int* sections, int n_axes, int interleaved, float eps, int dtype) {
@@ -61,12 +89,10 @@ int rope_chunk(int64_t rows, int tokens_per_warp, int H, int per_sm, int sms) {
 
 template <typename T, int D, bool PAGED>
 fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
-  const int sms = sm_count();
-  if (sms <= 0) return FA_ERR_CUDA;
   const int64_t tokens = int64_t(prm.B) * prm.N;
   constexpr int TOKENS = rope::Cfg<D>::TOKENS;
   const int heads = prm.Hq + (PAGED ? 2 : 1) * prm.Hkv;
-  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.Hq, FA_ROPE_PERSM, sms);
+  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.Hq, FA_ROPE_PERSM, kSms);
   prm.chunks_q = (prm.Hq + prm.chunk - 1) / prm.chunk;
   prm.chunks_k = (prm.Hkv + prm.chunk - 1) / prm.chunk;
   const int64_t units = (tokens + TOKENS - 1) / TOKENS * (prm.chunks_q + (PAGED ? 2 : 1) * prm.chunks_k);
@@ -74,8 +100,9 @@ fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
   if (tokens > 0x7fffff00 || grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
   auto kern = inter ? fa_qk_norm_rope_kernel<T, D, true, PAGED> : fa_qk_norm_rope_kernel<T, D, false, PAGED>;
   constexpr int SMEM = rope::STAGES * rope::Slot<T, sizeof(T) == 4>::BYTES;
-  if (set_smem(kern, SMEM) != cudaSuccess) return FA_ERR_CUDA;
-  if (launch_pdl(kern, dim3(unsigned(grid)), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess) return FA_ERR_CUDA;
+  static Prepared prepared[2];
+  if (prepared[inter].launch(kern, dim3(unsigned(grid)), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
+    return FA_ERR_CUDA;
   return launched();
 }
 
@@ -100,8 +127,8 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
   auto kern = inter ? fa_qk_norm_rope_bwd_kernel<T, TG, TO, D, true> : fa_qk_norm_rope_bwd_kernel<T, TG, TO, D, false>;
   constexpr int SMEM = rope::BWD_STAGES * rope::THREADS * 16 * int(sizeof(T) + sizeof(TG));
   static_assert(SMEM >= WARPS * D * 4, "the weight-gradient sums reuse the slots");
-  if (set_smem(kern, SMEM) != cudaSuccess) return FA_ERR_CUDA;
-  if (launch_pdl(kern, dim3(unsigned(ctas[0] + ctas[1])), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
+  static Prepared prepared[2];
+  if (prepared[inter].launch(kern, dim3(unsigned(ctas[0] + ctas[1])), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
     return FA_ERR_CUDA;
   if (prm.w[0] && launch_pdl(fa_qk_norm_rope_dw_kernel, dim3(D / 8, 2), dim3(512), 0, st,
                              static_cast<const float*>(prm.part), dwq, dwk, D, ctas[0], ctas[0] + ctas[1]) !=
@@ -192,18 +219,6 @@ bool part_sizes(int R, int Hq, int Hkv, int d, int max_blocks, int block_size) {
   return R > 0 && Hq > 0 && Hkv > 0 && d > 0 && max_blocks > 0 && block_size > 0 && Hq % Hkv == 0;
 }
 
-template <int D, bool PREFIX, bool SCORED>
-fa_status part_launch(const CUtensorMap& mk, const CUtensorMap& mv, const PartParams& prm, dim3 grid, cudaStream_t st) {
-  auto kern = fa_decode_part_kernel<D, PREFIX, SCORED>;
-  if (set_smem(kern, part::Cfg<D>::SMEM) != cudaSuccess ||
-      cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
-          cudaSuccess)
-    return FA_ERR_CUDA;
-  if (launch_pdl(kern, grid, dim3(part::WARPS * 32), part::Cfg<D>::SMEM, st, mk, mv, prm) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return FA_OK;
-}
-
 template <int D>
 fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const PartParams& prm, const PartPlan& n,
                         cudaStream_t st) {
@@ -215,11 +230,8 @@ fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const Part
                         prm.Hkv, G, n.RT, n.pairs * prm.Hkv, n.pairs, n.pre_parts, prm.prefix_blocks, prm.num_blocks,
                         prm.scale_log2, prm.wait_ns};
   // (all of the SM's memory as shared memory: the CTA of the next grid has to find room beside this one)
-  if (set_smem(fa_prefix_kernel<D>, C::SMEM) != cudaSuccess ||
-      cudaFuncSetAttribute(fa_prefix_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-    return FA_ERR_CUDA;
-  if (launch_pdl(fa_prefix_kernel<D>, dim3(part::PREFIX_CTAS), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, pp) !=
+  static Prepared prepared;
+  if (prepared.launch(fa_prefix_kernel<D>, dim3(part::PREFIX_CTAS), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, pp) !=
       cudaSuccess)
     return FA_ERR_CUDA;
   return FA_OK;
@@ -228,19 +240,19 @@ fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const Part
 template <int D>
 fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm, const PartPlan& n, bool scored,
                    cudaStream_t st) {
-  fa_status s = FA_OK;
   if (prm.pre_o) {
-    s = prefix_launch<D>(mk, mv, prm, n, st);
-#ifndef FA_NO_LATE
+    const fa_status s = prefix_launch<D>(mk, mv, prm, n, st);
+    if (s != FA_OK) return s;
     prm.late_wait = true;
-#endif
-  } else if (prm.pbt) {
-    s = part_launch<D, true, false>(mk, mv, prm, dim3(n.prefix_parts, prm.Hkv, n.row_tiles), st);
   }
-  if (s != FA_OK) return s;
-  const dim3 own(n.own_parts, prm.Hkv, prm.R);
-  s = scored ? part_launch<D, false, true>(mk, mv, prm, own, st) : part_launch<D, false, false>(mk, mv, prm, own, st);
-  if (s != FA_OK) return s;
+  const int64_t pre = int64_t(n.prefix_parts) * prm.Hkv * n.row_tiles, own = int64_t(n.own_parts) * prm.Hkv * prm.R;
+  if (pre + own > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  prm.n_prefix = int(pre);
+  static Prepared prepared[2];
+  auto kern = scored ? fa_decode_part_kernel<D, true> : fa_decode_part_kernel<D, false>;
+  if (prepared[scored].launch(kern, dim3(unsigned(pre + own)), dim3(part::WARPS * 32), part::Cfg<D>::SMEM, st, mk, mv,
+                              prm) != cudaSuccess)
+    return FA_ERR_CUDA;
   // warps that share a row of the join: one for each 8 pieces it may have
   const int most = n.own_parts + n.prefix_parts + n.pre_parts;
   const int strands = most > 32 ? 8 : most > 16 ? 4 : most > 8 ? 2 : 1;
@@ -285,7 +297,7 @@ fa_status part_call(const void* q, const void* k_cache, const void* v_cache, con
   PartParams prm{static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(o), lse,
                  reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + n.off_lse),
                  reinterpret_cast<float*>(ws + n.off_scores), weights, block_table, ctx_lens, prefix_table, prefix_len,
-                 R, Hq, Hkv, max_blocks, max_prefix_blocks, num_blocks, n.own_parts + n.prefix_parts, n.prefix_parts,
+                 R, Hq, Hkv, max_blocks, max_prefix_blocks, num_blocks, n.own_parts + n.prefix_parts, n.prefix_parts, n.own_parts, 0,
                  n.chunk, n.prefix_chunk,
                  n.pairs > 0 ? reinterpret_cast<const float*>(ws + n.off_pre_o) : nullptr,
                  n.pairs > 0 ? reinterpret_cast<const float*>(ws + n.off_pre_lse) : nullptr,
@@ -526,8 +538,8 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t M = int64_t(a.max_blocks_per_seq) * evict::BS;
   const int smem = n.in_smem ? int((M + 2 * ((M + 31) / 32)) * 4) : 0;
-  if (smem > 8192 && set_smem(fa_evict_select_kernel, smem) != cudaSuccess) return FA_ERR_CUDA;
-  if (launch_pdl(fa_evict_select_kernel, dim3(a.Hkv, a.R), dim3(evict::THREADS), smem, st, prm) != cudaSuccess)
+  static Prepared prepared;
+  if (prepared.launch(fa_evict_select_kernel, dim3(a.Hkv, a.R), dim3(evict::THREADS), smem, st, prm) != cudaSuccess)
     return FA_ERR_CUDA;
   if (!n.fused && n.cap > 0) {
     const int64_t pieces = int64_t(n.cap) * 2 * prm.row16;
