@@ -8,15 +8,6 @@
 #ifndef FA_PREFIX_ROWS
 #define FA_PREFIX_ROWS 64
 #endif
-#ifndef FA_ROPE_PERSM
-#define FA_ROPE_PERSM 32
-#endif
-#ifndef FA_ROPE_BWD_PERSM
-#define FA_ROPE_BWD_PERSM 32
-#endif
-#ifndef FA_ROPE_BWD_C
-#define FA_ROPE_BWD_C 2
-#endif
 
 namespace {
 
@@ -78,6 +69,28 @@ bool rope_rows(const void* p, const int64_t* strides, int dtype) {
   return true;
 }
 
+template <typename T, int D, bool PAGED>
+fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
+  const int64_t tokens = int64_t(prm.B) * prm.N;
+  constexpr int TOKENS = rope::Cfg<D>::TOKENS;
+  const int heads = prm.Hq + (PAGED ? 2 : 1) * prm.Hkv;
+  // Warps that share a token group: about 10 heads each, and all eight while that leaves
+  // SMs without a CTA.
+  const int64_t tgroups = (tokens + TOKENS - 1) / TOKENS;
+  int sharers = 8;
+  while (sharers > 1 && heads < 10 * sharers && tgroups * (sharers / 2) >= int64_t(8) * 4 * kSms) sharers /= 2;
+  prm.groups = 8 / sharers;
+  const int64_t grid = (tgroups + prm.groups - 1) / prm.groups;
+  if (tokens > 0x7fffff00 || grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  auto kern = inter ? fa_qk_norm_rope_kernel<T, D, true, PAGED> : fa_qk_norm_rope_kernel<T, D, false, PAGED>;
+  const int smem = (sizeof(T) == 4 ? FA_ROPE_STAGES_F32 : FA_ROPE_STAGES) * rope::Slot<T, sizeof(T) == 4>::BYTES +
+                   (prm.groups * rope::TABLE + 8 * rope::Cfg<D>::L) * 16;
+  static Prepared prepared[2];
+  if (prepared[inter].launch(kern, dim3(unsigned(grid)), dim3(rope::THREADS), smem, st, prm) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return launched();
+}
+
 // Heads per unit of work: 16, halved until every SM has `per_sm` units (or a head is a unit),
 // and spread evenly over the heads.
 int rope_chunk(int64_t rows, int tokens_per_warp, int H, int per_sm, int sms) {
@@ -87,26 +100,7 @@ int rope_chunk(int64_t rows, int tokens_per_warp, int H, int per_sm, int sms) {
   return (H + chunks - 1) / chunks;
 }
 
-template <typename T, int D, bool PAGED>
-fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
-  const int64_t tokens = int64_t(prm.B) * prm.N;
-  constexpr int TOKENS = rope::Cfg<D>::TOKENS;
-  const int heads = prm.Hq + (PAGED ? 2 : 1) * prm.Hkv;
-  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.Hq, FA_ROPE_PERSM, kSms);
-  prm.chunks_q = (prm.Hq + prm.chunk - 1) / prm.chunk;
-  prm.chunks_k = (prm.Hkv + prm.chunk - 1) / prm.chunk;
-  const int64_t units = (tokens + TOKENS - 1) / TOKENS * (prm.chunks_q + (PAGED ? 2 : 1) * prm.chunks_k);
-  const int64_t grid = (units + rope::THREADS / 32 - 1) / (rope::THREADS / 32);
-  if (tokens > 0x7fffff00 || grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  auto kern = inter ? fa_qk_norm_rope_kernel<T, D, true, PAGED> : fa_qk_norm_rope_kernel<T, D, false, PAGED>;
-  constexpr int SMEM = rope::STAGES * rope::Slot<T, sizeof(T) == 4>::BYTES;
-  static Prepared prepared[2];
-  if (prepared[inter].launch(kern, dim3(unsigned(grid)), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return launched();
-}
-
-constexpr int kRopeBwdCtas = 148 * FA_ROPE_BWD_C;  // CTAs of the backward kernel, at most
+constexpr int kRopeBwdCtas = kSms * 2;  // CTAs of the backward kernel, at most
 
 template <typename T, typename TG, typename TO, int D>
 fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk, cudaStream_t st) {
@@ -114,7 +108,7 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
   if (tokens > 0x7fffff00) return FA_ERR_UNSUPPORTED;
   constexpr int TOKENS = rope::Cfg<D>::TOKENS, WARPS = rope::THREADS / 32;
   const int heads = prm.H[0] + prm.H[1];
-  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.H[0], FA_ROPE_BWD_PERSM, kRopeBwdCtas / FA_ROPE_BWD_C);
+  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.H[0], 32, kSms);
   int ctas[2];
   for (int k = 0; k < 2; ++k) {
     prm.chunks[k] = (prm.H[k] + prm.chunk - 1) / prm.chunk;
@@ -353,7 +347,7 @@ fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* args, void* stream) {
                  a.positions, a.inv_freq,
                  {a.q_out, a.k_out},
                  a.pos_axis_stride, a.pos_batch_stride, a.B, a.Hq, a.Hkv, a.N, a.rotary_dim, a.sections[0],
-                 a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1, 1, 1,
+                 a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1,
                  nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a.dtype == FA_DTYPE_BF16 ? rope_by_d<__nv_bfloat16>(prm, a.d, a.interleaved, st)
@@ -386,7 +380,7 @@ fa_status fa_qk_norm_rope_append(const fa_qk_norm_rope_append_args* args, void* 
                  a.positions, a.inv_freq,
                  {a.q_out, nullptr},
                  a.pos_axis_stride, a.pos_batch_stride, a.R, a.Hq, a.Hkv, a.Nq_max, a.rotary_dim, a.sections[0],
-                 a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1, 1, 1,
+                 a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1,
                  a.block_table, a.ctx_lens, a.q_lens, a.k_cache, a.v_cache, a.max_blocks_per_seq, a.num_blocks};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (a.d) {

@@ -10,11 +10,13 @@
 // What bounds it: device memory.  Each value is read once and written once (backward: dy and x
 // read, dx written) for about 10 operations.  A row of d values is held by d/16 lanes, four runs
 // of 4 values each, chosen so that both members of every pair sit in one lane: no value moves
-// between lanes but the row's sum of squares.  A group of lanes stays with one token and walks
-// heads: the token's cosines and sines and the head weights are computed and read once and stay
-// in registers, there is no shared memory and no barrier, and a warp writes 1 KB of consecutive
-// tokens of one head.  `chunk` heads make a unit of work, few when there are few tokens (a
-// decode step then has a row per group) and up to MAX_CHUNK, which amortises the cosines.
+// between lanes but the row's sum of squares.  Forward: a CTA takes the tokens of 1 to 8 warps (a
+// warp holds 32 / lanes tokens of one head) with all their heads.  Each thread computes one cosine
+// and sine per token group, while the first rows are on their way; all heads' rows share them,
+// from shared memory, as they share the weights.  (With the angles of a lane's 8 pairs computed by
+// each warp for itself and kept in registers, 116 registers left 16 warps on an SM, and the
+// 8192-token prefill of 4 x 40 heads took 115 us instead of @@.)  A warp writes 1 KB of
+// consecutive tokens of one head.
 //
 // Angles: the position (up to 2^31) times the frequency is taken in turns in 64 bits and reduced
 // to [-1/2, 1/2] before it is rounded to 32 bits, so far positions lose nothing; no table of
@@ -26,8 +28,11 @@ namespace fa {
 #ifndef FA_ROPE_STAGES
 #define FA_ROPE_STAGES 5
 #endif
+#ifndef FA_ROPE_STAGES_F32
+#define FA_ROPE_STAGES_F32 4
+#endif
 #ifndef FA_ROPE_MINB
-#define FA_ROPE_MINB 2
+#define FA_ROPE_MINB 3
 #endif
 #ifndef FA_ROPE_BWD_STAGES
 #define FA_ROPE_BWD_STAGES 4
@@ -37,9 +42,8 @@ namespace fa {
 #endif
 namespace rope {
 constexpr int THREADS = 256;
-constexpr int MAX_CHUNK = 16;  // heads of a unit, at most
-constexpr int STAGES = FA_ROPE_STAGES;          // forward: rows a thread has in flight, + 1
-constexpr int BWD_STAGES = FA_ROPE_BWD_STAGES;  // backward
+constexpr int MAX_CHUNK = 16;  // backward: heads of a unit, at most
+constexpr int BWD_STAGES = FA_ROPE_BWD_STAGES;  // backward: rows a thread has in flight, + 1
 
 // Lanes of one row: d / 16 rounded up to a power of two (d = 96: 6 of 8 lanes work).
 template <int D>
@@ -61,8 +65,7 @@ struct RopeParams {
   int B, Hq, Hkv, N;
   int rd, sec0, sec1;     // rotary dims; frequencies below sec0 follow axis 0, below sec1 axis 1, then axis 2
   float eps;
-  int chunk;              // heads per unit
-  int chunks_q, chunks_k; // units of a token group: of q, of k (and as many of v)
+  int groups;             // token groups of a CTA: 1, 2, 4 or 8; 8 / groups warps share one
   // paged: cache rows of the tokens
   const int *bt, *ctx, *qlen;
   void *kc, *vc;
@@ -83,7 +86,7 @@ struct RopeBwdParams {
   int B, H[2], N;
   int rd, sec0, sec1;
   float eps;
-  int chunk, chunks[2];
+  int chunk, chunks[2];  // heads per unit; units of a token group, of q and of k
   int ctas_q;  // CTAs [0, ctas_q) take the rows of q, the others those of k
 };
 
@@ -222,6 +225,47 @@ __device__ __forceinline__ void angles(const Runs<D, SPREAD>& r, const int* pos,
   }
 }
 
+// Cosines and sines of the 8 pairs of every lane, for one token group, in shared memory: one
+// float4 a lane in four planes (a 16-byte read of neighbouring lanes touches neighbouring banks),
+// cosines of pairs 0-3 and 4-7, then sines.  Pairs behind the rotary width get 1 and 0.  `pos`
+// points at the token's position on axis 0.
+constexpr int TABLE = 4 * 32;  // float4 of a token group
+template <bool INTER, int D, bool SPREAD>
+__device__ __forceinline__ void table_entry(float4* table, int lane, int e, const Runs<D, SPREAD>& r, const int* pos,
+                                            int64_t pos_sa, const double* freq, int rd, int sec0, int sec1, bool on) {
+  float s = 0.f, c = 1.f;
+  if (on && r.q[0] * 4 < rd) {
+    const int f = INTER ? r.q[e >> 1] * 2 + (e & 1) : r.q[e >> 2] * 4 + (e & 3);
+    const int axis = f < sec0 ? 0 : f < sec1 ? 1 : 2;
+    const double turns = double(__ldg(pos + axis * pos_sa)) * (__ldg(freq + f) * 0.15915494309189533577);
+    sincospif(2.f * float(turns - rint(turns)), &s, &c);
+  }
+  float* at = reinterpret_cast<float*>(table + (e >> 2) * 32 + lane) + (e & 3);
+  at[0] = c;
+  at[2 * 32 * 4] = s;
+}
+// One kind's weights in the same form: [4][L].
+template <typename T, int D, bool SPREAD>
+__device__ __forceinline__ void fill_weights(float4* table, const void* w, int rd) {
+  using C = Cfg<D>;
+  for (int i = threadIdx.x; i < C::PAIRS * 16; i += THREADS) {  // value v of lane l
+    const int l = i / 16, v = i % 16;
+    const Runs<D, SPREAD> r(l, rd);
+    reinterpret_cast<float*>(table + (v >> 2) * C::L + l)[v & 3] =
+        float(static_cast<const T*>(w)[r.q[v >> 2] * 4 + (v & 3)]);
+  }
+}
+// 8 pairs (16 values), or 4, from planes of float4.
+template <int N>
+__device__ __forceinline__ void read_planes(const float4* t, int stride, float2 (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float4 v = t[i * stride];
+    f[2 * i] = make_float2(v.x, v.y);
+    f[2 * i + 1] = make_float2(v.z, v.w);
+  }
+}
+
 // Turn a lane's pairs: half-width pairs (runs 0, 1 with runs 2, 3) in packed form, adjacent ones
 // one by one.
 template <bool INTER>
@@ -252,32 +296,31 @@ __device__ __forceinline__ float row_sum(float v) {
 
 }  // namespace rope
 
-// One warp per unit: 32 / L consecutive tokens (of the B x N) x `chunk` heads of q, k or v.
 // PAGED (bf16): token (r, i) of request r is one of its last q_lens[r] positions; q' goes to
 // [R, Hq, N, d], k' and v to cache position ctx_lens[r] - q_lens[r] + i; padding rows are left.
 template <typename T, int D, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB) fa_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB)
+    fa_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   using namespace rope;
   using C = Cfg<D>;
+  constexpr bool SPREAD = sizeof(T) == 4;
+  constexpr int STAGES = SPREAD ? FA_ROPE_STAGES_F32 : FA_ROPE_STAGES;
+  using R = Slot<T, SPREAD>;
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  float4* s_table = reinterpret_cast<float4*>(rope_smem + STAGES * R::BYTES);  // [groups][TABLE]
+  float4* s_w = s_table + p.groups * TABLE;                                    // [q, k][4][L]
   const int tokens = p.B * p.N;
-  const int per_group = p.chunks_q + (PAGED ? 2 : 1) * p.chunks_k;
-  const int64_t unit = int64_t(blockIdx.x) * (THREADS / 32) + warp_id();
-  const int tg = int(unit / per_group);
-  int chunk = int(unit - int64_t(tg) * per_group);
-  const int lane = lane_id(), c = lane % C::L;
-  const int t = tg * C::TOKENS + lane / C::L;
-  if (tg * C::TOKENS >= tokens) return;  // (the whole warp)
-  const int kind = chunk < p.chunks_q ? 0 : chunk < p.chunks_q + p.chunks_k ? 1 : 2;
-  if (kind > 0) chunk -= p.chunks_q + (kind - 1) * p.chunks_k;
-  const int H = kind == 0 ? p.Hq : p.Hkv;
-  const int h0 = chunk * p.chunk, h1 = min(H, h0 + p.chunk);
+  const int lane = lane_id(), c = lane % C::L, warp = warp_id();
+  const int sharers = 8 / p.groups, sub = warp / sharers;  // warps of a token group; this warp's group
+  const int t = (int(blockIdx.x) * p.groups + sub) * C::TOKENS + lane / C::L;
+  const int heads = p.Hq + p.Hkv + (PAGED ? p.Hkv : 0);
   bool on = c < C::PAIRS && t < tokens;
   const int b = on ? t / p.N : 0, n = on ? t - b * p.N : 0;
-  constexpr bool SPREAD = sizeof(T) == 4;
   const Runs<D, SPREAD> runs(c < C::PAIRS ? c : 0, p.rd);
+  const bool norm = p.w[0] != nullptr;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int64_t row = 0;  // paged: cache row (block * Hkv * 16 + slot) of the token
+  int phys = 0, at = 0;  // paged: cache block and position of the token
   if constexpr (PAGED) {
     if (on) {
       const int L = p.ctx[b], ql = p.qlen[b];
@@ -286,62 +329,87 @@ __global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB) fa_qk_norm_rope_k
         on = false;
       } else if (n >= ql) {
         on = false;
-      } else if (kind > 0) {
-        const int at = L - ql + n;
-        const int phys = p.bt[int64_t(b) * p.max_blocks + at / 16];
-        if (phys < 0 || phys >= p.num_blocks) {
-          set_status(FA_ERR_INVALID_ARG, 201);
-          on = false;
-        } else {
-          row = int64_t(phys) * p.Hkv * 16 + at % 16;
-        }
+      } else {
+        at = L - ql + n;
+        phys = p.bt[int64_t(b) * p.max_blocks + at / 16];
       }
     }
-    if (!__any_sync(0xffffffffu, on)) return;
   }
-  const T* src = static_cast<const T*>(p.x[kind]) + b * p.sb[kind] + n * p.sn[kind];
-  const int64_t sh = p.sh[kind];
-  T* dst;
-  int64_t dh;  // distance of two heads' rows
-  if (PAGED && kind > 0) {
-    dst = static_cast<T*>(kind == 1 ? p.kc : p.vc) + row * D;
-    dh = 16 * D;
-  } else {
-    dst = static_cast<T*>(p.out[kind == 0 ? 0 : 1]) + (int64_t(b) * H * p.N + n) * D;
-    dh = int64_t(p.N) * D;
-  }
-  // rows in flight: prologue, then one more for each row that is worked on
-  using R = Slot<T, SPREAD>;
-  extern __shared__ uint8_t rope_smem[];
   const uint32_t slot = smem_u32(rope_smem) + threadIdx.x * R::PIECE;
+  const int h0 = warp - sub * sharers;
+  int64_t off[PAGED ? 3 : 2];
+#pragma unroll
+  for (int k = 0; k < (PAGED ? 3 : 2); ++k) off[k] = b * p.sb[k] + n * p.sn[k];
+  // row i of this warp: head h0 + i * sharers of q, then k, then v
   auto fetch = [&](int i) {
-    if (h0 + i < h1) R::template fetch<D>(slot + (i % STAGES) * R::BYTES, src + (h0 + i) * sh, runs, on);
+    const int h = h0 + i * sharers;
+    if (h < heads) {
+      const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
+      const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
+      const T* src = static_cast<const T*>(p.x[kind]) + (kind == 0 ? off[0] : kind == 1 ? off[1] : off[PAGED ? 2 : 1]);
+      R::template fetch<D>(slot + (i % STAGES) * R::BYTES, src + hh * p.sh[kind], runs, on);
+    }
     rows_commit();
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(i);
-  const bool norm = kind < 2 && p.w[0] != nullptr;
-  float2 w[8], cs[4], sn[4];
-  if (on && kind < 2) {
-    if (norm) load_weights<T>(p.w[kind], runs, w);
-    angles<INTER>(runs, p.pos + b * p.pos_sb + n, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, cs, sn);
+  // meanwhile the tables: thread (pair warp, lane) of every token group
+  for (int g = 0; g < p.groups; ++g) {
+    const int tt = (int(blockIdx.x) * p.groups + g) * C::TOKENS + lane / C::L;
+    const int bb = tt < tokens ? tt / p.N : 0, nn = tt < tokens ? tt - bb * p.N : 0;
+    table_entry<INTER>(s_table + g * TABLE, lane, warp, runs, p.pos + bb * p.pos_sb + nn, p.pos_sa, p.freq, p.rd, p.sec0,
+                       p.sec1, c < C::PAIRS && tt < tokens);
   }
-  for (int i = 0; h0 + i < h1; ++i) {
+  if (norm) {
+    fill_weights<T, D, SPREAD>(s_w, p.w[0], p.rd);
+    fill_weights<T, D, SPREAD>(s_w + 4 * C::L, p.w[1], p.rd);
+  }
+  int64_t row = -1;  // cache row (block * Hkv * 16 + slot) of the token, -1: not cached
+  if constexpr (PAGED) {
+    if (on && (phys < 0 || phys >= p.num_blocks))
+      set_status(FA_ERR_INVALID_ARG, 201);
+    else
+      row = int64_t(phys) * p.Hkv * 16 + at % 16;
+    if (!__syncthreads_or(on)) {
+      rows_wait<0>();
+      return;
+    }
+  } else {
+    __syncthreads();
+  }
+  const float4* table = s_table + sub * TABLE + lane;
+  for (int i = 0; h0 + i * sharers < heads; ++i) {
     rows_wait<STAGES - 2>();
     float2 f[8];
     R::read(slot + (i % STAGES) * R::BYTES, f);
     fetch(i + STAGES - 1);  // into the slot of row i - 1
-    if (norm) {
-      float2 sq = mul2(f[0], f[0]);
+    const int h = h0 + i * sharers;
+    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
+    const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
+    if (kind < 2) {
+      if (norm) {
+        float2 sq = mul2(f[0], f[0]);
 #pragma unroll
-      for (int e = 1; e < 8; ++e) sq = fma2(f[e], f[e], sq);
-      const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
+        for (int e = 1; e < 8; ++e) sq = fma2(f[e], f[e], sq);
+        const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
+        float2 w[8];
+        read_planes(s_w + kind * 4 * C::L + (c < C::PAIRS ? c : 0), C::L, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2(r, w[e]));
+        for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2(r, w[e]));
+      }
+      float2 cs[4], sn[4];
+      read_planes(table, 32, cs);
+      read_planes(table + 2 * 32, 32, sn);
+      turn<INTER>(f, cs, sn);
     }
     if (on) {
-      if (kind < 2) turn<INTER>(f, cs, sn);
-      store_row(dst + (h0 + i) * dh, runs, f);
+      if (kind == 0) {
+        store_row(static_cast<T*>(p.out[0]) + ((int64_t(b) * p.Hq + hh) * p.N + n) * D, runs, f);
+      } else if constexpr (PAGED) {
+        if (row >= 0) store_row(static_cast<T*>(kind == 1 ? p.kc : p.vc) + (row + hh * 16) * D, runs, f);
+      } else {
+        store_row(static_cast<T*>(p.out[1]) + ((int64_t(b) * p.Hkv + hh) * p.N + n) * D, runs, f);
+      }
     }
   }
 }
