@@ -413,7 +413,7 @@ def _like_rows(t, B, H, N, d, dtype):
     """An empty [B,H,N,d] tensor: as [B,N,H,d] in memory where t is a view of a projection, else contiguous."""
     strides = t.stride()
     if strides[2] > strides[1]:
-        return t.new_empty((B, N, H, d), dtype=dtype).transpose(1, 2)
+        return torch.empty_strided((B, H, N, d), (N * H * d, d, H * d, 1), dtype=dtype, device=t.device)
     return t.new_empty((B, H, N, d), dtype=dtype)
 
 

@@ -20,7 +20,10 @@
 namespace fa {
 namespace part {
 constexpr int WARPS = 4;
-constexpr int STAGES = 2;
+#ifndef FA_PART_STAGES
+#define FA_PART_STAGES 2
+#endif
+constexpr int STAGES = FA_PART_STAGES;
 constexpr int BS = 16;
 constexpr int ROWS = 16;       // query rows of a piece
 constexpr int MIN_CHUNK = 8;   // blocks of a piece, at least: two for each warp

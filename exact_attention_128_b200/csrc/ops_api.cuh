@@ -91,15 +91,6 @@ fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
   return launched();
 }
 
-// Heads per unit of work: 16, halved until every SM has `per_sm` units (or a head is a unit),
-// and spread evenly over the heads.
-int rope_chunk(int64_t rows, int tokens_per_warp, int H, int per_sm, int sms) {
-  int c = rope::MAX_CHUNK;
-  while (c > 1 && rows / (int64_t(tokens_per_warp) * c) < int64_t(per_sm) * sms) c /= 2;
-  const int chunks = (H + c - 1) / c;
-  return (H + chunks - 1) / chunks;
-}
-
 constexpr int kRopeBwdCtas = kSms * 2;  // CTAs of the backward kernel, at most
 
 template <typename T, typename TG, typename TO, int D>
@@ -107,16 +98,39 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
   const int64_t tokens = int64_t(prm.B) * prm.N;
   if (tokens > 0x7fffff00) return FA_ERR_UNSUPPORTED;
   constexpr int TOKENS = rope::Cfg<D>::TOKENS, WARPS = rope::THREADS / 32;
-  const int heads = prm.H[0] + prm.H[1];
-  prm.chunk = rope_chunk(tokens * heads, TOKENS, prm.H[0], 32, kSms);
-  int ctas[2];
-  for (int k = 0; k < 2; ++k) {
-    prm.chunks[k] = (prm.H[k] + prm.chunk - 1) / prm.chunk;
-    // CTAs in proportion to the rows, no more than there are units
-    const int64_t units = (tokens + TOKENS - 1) / TOKENS * prm.chunks[k];
-    const int64_t share = std::max<int64_t>(1, int64_t(kRopeBwdCtas) * prm.H[k] / heads);
-    ctas[k] = int(std::min<int64_t>(std::min<int64_t>(share, kRopeBwdCtas - 1), (units + WARPS - 1) / WARPS));
-  }
+  // Heads per unit and CTAs of q and of k: units go to warps in turn, so the slowest warp has
+  // ceil(units / warps) of them, each worth its heads and about two more for its cosines.  Of all
+  // ways to cut the heads, the one whose slowest warp is the fastest.
+  const int64_t tgroups = (tokens + TOKENS - 1) / TOKENS;
+  int64_t best = INT64_MAX;
+  int ctas[2] = {1, 1};
+  for (int cq = rope::MAX_CHUNK; cq >= 1; cq /= 2)
+    for (int ck = rope::MAX_CHUNK; ck >= 1; ck /= 2) {
+      const int most[2] = {cq, ck};
+      int chunk[2], chunks[2], n[2];
+      int64_t units[2], work[2], time = 0;
+      for (int k = 0; k < 2; ++k) {
+        chunks[k] = (prm.H[k] + most[k] - 1) / most[k];
+        chunk[k] = (prm.H[k] + chunks[k] - 1) / chunks[k];
+        units[k] = tgroups * chunks[k];
+        work[k] = units[k] * (chunk[k] + 2);
+      }
+      for (int k = 0; k < 2; ++k) {
+        const int64_t share = int64_t(double(kRopeBwdCtas) * double(work[k]) / double(work[0] + work[1]) + 0.5);
+        n[k] = int(std::min<int64_t>(std::max<int64_t>(1, std::min<int64_t>(kRopeBwdCtas - 1, share)),
+                                     (units[k] + WARPS - 1) / WARPS));
+        time = std::max(time, (units[k] + n[k] * WARPS - 1) / (n[k] * WARPS) * (chunk[k] + 2));
+      }
+      if (n[0] + n[1] > kRopeBwdCtas) --n[n[0] > n[1] ? 0 : 1];  // (both shares rounded up)
+      if (time < best) {
+        best = time;
+        for (int k = 0; k < 2; ++k) {
+          prm.chunk[k] = chunk[k];
+          prm.chunks[k] = chunks[k];
+          ctas[k] = n[k];
+        }
+      }
+    }
   prm.ctas_q = ctas[0];
   auto kern = inter ? fa_qk_norm_rope_bwd_kernel<T, TG, TO, D, true> : fa_qk_norm_rope_bwd_kernel<T, TG, TO, D, false>;
   constexpr int SMEM = rope::BWD_STAGES * rope::THREADS * 16 * int(sizeof(T) + sizeof(TG));
@@ -434,7 +448,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream
                     {a.dq_strides[2], a.dk_strides[2]},
                     static_cast<float*>(a.workspace),
                     a.pos_axis_stride, a.pos_batch_stride, a.B, {a.Hq, a.Hkv}, a.N, a.rotary_dim, a.sections[0],
-                    a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, 1, {1, 1}, 0};
+                    a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, {1, 1}, {1, 1}, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.dtype == FA_DTYPE_F32) return rope_bwd_by_d<float, float, float>(prm, a.d, a.interleaved, a.dq_weight,
       a.dk_weight, st);

@@ -86,7 +86,7 @@ struct RopeBwdParams {
   int B, H[2], N;
   int rd, sec0, sec1;
   float eps;
-  int chunk, chunks[2];  // heads per unit; units of a token group, of q and of k
+  int chunk[2], chunks[2];  // of q and of k: heads per unit, units of a token group
   int ctas_q;  // CTAs [0, ctas_q) take the rows of q, the others those of k
 };
 
@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(rope::THREADS, FA_ROPE_BWD_MINB) fa_qk_norm_ro
   if (norm) load_weights<T>(p.w[kind], runs, w);
 
   for (int64_t unit = int64_t(cta) * (THREADS / 32) + warp_id(); unit < units; unit += int64_t(n_cta) * (THREADS / 32)) {
-    const int tg = int(unit / chunks), h0 = int(unit - int64_t(tg) * chunks) * p.chunk, h1 = min(H, h0 + p.chunk);
+    const int tg = int(unit / chunks), h0 = int(unit - int64_t(tg) * chunks) * p.chunk[kind],
+              h1 = min(H, h0 + p.chunk[kind]);
     const int t = tg * C::TOKENS + lane / C::L;
     const bool on = c < C::PAIRS && t < tokens;
     const int b = on ? t / p.N : 0, n = on ? t - b * p.N : 0;
