@@ -28,6 +28,21 @@
 
 namespace fa {
 
+// All N phases: the barriers are looked at together, since a look takes some 200 cycles even where
+// the phase is over (one after the other, six of them took half of a step's 2500 cycles).
+template <int N>
+__device__ __forceinline__ bool warp_wait_all(uint64_t* const (&bar)[N], const uint32_t (&parity)[N], uint64_t limit_ns,
+                                              volatile int* abort_flag, int where) {
+  bool over = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) over &= mbar_try_wait(bar[i], parity[i]);
+  if (__all_sync(0xffffffffu, over)) return true;
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) ok = ok && warp_wait(bar[i], parity[i], limit_ns, abort_flag, where + i);
+  return ok;
+}
+
 template <int D>
 struct PrefixCfg {
   static constexpr int BM = 128, BN = PrefixDeal::BN;
@@ -221,10 +236,6 @@ __global__ void __launch_bounds__(608)
     // The scores of a step go where P of two steps before was.  The tensor core keeps the order of
     // MMAs of one shape and accumulator only, so that step's P V must be waited for.  pv_done is
     // waited for once per step, in order: a barrier two phases ahead would look incomplete.
-    auto pv_complete = [&](int s) {
-      return s < 0 || (warp_wait(&bars->pv_done[0], s & 1, p.wait_ns, abort_flag, 326) &&
-                       warp_wait(&bars->pv_done[1], s & 1, p.wait_ns, abort_flag, 327));
-    };
     for (long long x = x0; x < x1 && ok; ++local) {
       const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
       const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
@@ -237,31 +248,37 @@ __global__ void __launch_bounds__(608)
       if (j1 - j0 == 1) mma_commit_p(&bars->q_empty, leader);
       for (int j = j0; j < j1; ++j, ++kv) {
         const int st = kv % C::NSTAGE;
-        if (!(ok = pv_complete(kv - 1))) break;
+        const int i = kv + 1, st2 = i % C::NSTAGE;
+        const uint32_t pk = (i / C::NSTAGE) & 1, pd = (kv - 1) & 1;
         if (j + 1 < j1) {
-          const int i = kv + 1;
-          if (!(ok = warp_wait(&bars->k_full[i % C::NSTAGE], (i / C::NSTAGE) & 1, p.wait_ns, abort_flag, 324))) break;
+          ok = kv > 0 ? warp_wait_all({&bars->k_full[st2], &bars->pv_done[0], &bars->pv_done[1]}, {pk, pd, pd}, p.wait_ns,
+                                      abort_flag, 324)
+                      : warp_wait(&bars->k_full[st2], pk, p.wait_ns, abort_flag, 324);
+          if (!ok) break;
           tc_fence_after();
           issue_S(i, i);
           if (j + 2 == j1) mma_commit_p(&bars->q_empty, leader);  // the item's last scores
+        } else if (kv > 0) {
+          if (!(ok = warp_wait_all({&bars->pv_done[0], &bars->pv_done[1]}, {pd, pd}, p.wait_ns, abort_flag, 325))) break;
         }
-        if (!(ok = warp_wait(&bars->v_full[st], (kv / C::NSTAGE) & 1, p.wait_ns, abort_flag, 322))) break;
+        const uint32_t pp = (kv >> 1) & 1;
+        ok = warp_wait_all({&bars->v_full[st], &bars->p_full[0][kv & 1], &bars->p_full[1][kv & 1]},
+                           {uint32_t((kv / C::NSTAGE) & 1), pp, pp}, p.wait_ns, abort_flag, 327);
+        if (!ok) break;
         if ((P & 15) != 0 && (P - 1) / C::BN == j) {  // V rows of the last block's unused slots: zero
           uint8_t* sv = smem + C::OFF_V + st * C::KV_TILE;
           const int r0 = P - j * C::BN, r1 = nblk * 16 - j * C::BN;
           for (int kb = 0; kb < C::KB; ++kb)
-            for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
-              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int z = r0 * 8 + lane; z < r1 * 8; z += 32)
+              *reinterpret_cast<uint4*>(sv + kb * C::BN * 128 + z * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (!(ok = warp_wait(&bars->p_full[t][kv & 1], (kv >> 1) & 1, p.wait_ns, abort_flag, 323 + 2 * t))) break;
-          tc_fence_after();
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
           issue_PV(t, st, kv, j == j0);
           if (j + 1 == j1) mma_commit_p(&bars->o_final[t], leader);
         }
-        if (!ok) break;
         mma_commit_p(&bars->v_empty[st], leader);
       }
     }
