@@ -33,10 +33,13 @@ namespace fa {
 template <int N>
 __device__ __forceinline__ bool warp_wait_all(uint64_t* const (&bar)[N], const uint32_t (&parity)[N], uint64_t limit_ns,
                                               volatile int* abort_flag, int where) {
-  bool over = true;
+#pragma unroll 1
+  for (int look = 0; look < 32; ++look) {
+    bool over = true;
 #pragma unroll
-  for (int i = 0; i < N; ++i) over &= mbar_try_wait(bar[i], parity[i]);
-  if (__all_sync(0xffffffffu, over)) return true;
+    for (int i = 0; i < N; ++i) over &= mbar_try_wait(bar[i], parity[i]);
+    if (__all_sync(0xffffffffu, over)) return true;
+  }
   bool ok = true;
 #pragma unroll
   for (int i = 0; i < N; ++i) ok = ok && warp_wait(bar[i], parity[i], limit_ns, abort_flag, where + i);
@@ -74,7 +77,7 @@ struct PrefixParams {
 struct PrefixBars {
   uint64_t q_full, q_empty, k_full[4], v_full[4], k_empty[4], v_empty[4];
   uint64_t s_full[2][2], p_full[2][2];  // [row tile][buffer]
-  uint64_t pv_done[2], o_final[2], drained;
+  uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -106,8 +109,6 @@ __global__ void __launch_bounds__(608)
         mbar_init(&bars->s_full[t][b], 1);
         mbar_init(&bars->p_full[t][b], 4);
       }
-      mbar_init(&bars->pv_done[t], 1);
-      mbar_init(&bars->o_final[t], 1);
     }
     mbar_init(&bars->drained, 1);
     bars->abort_flag = 0;
@@ -229,13 +230,12 @@ __global__ void __launch_bounds__(608)
       for (int ks = 0; ks < C::BN / 16; ++ks)
         mma_ts_p(tmem + C::COL_O + t * D, tmem + (2 * (g & 1) + t) * C::BN + ks * 8,
                  desc_add(dV, st * C::KV_TILE + ks * 16 * 128), idPV, (!first || ks > 0) ? 1u : 0u, leader);
-      mma_commit_p(&bars->pv_done[t], leader);
     };
     int kv = 0, local = 0;  // kv: K/V tiles so far, which is also the step (every tile is one)
     bool ok = true;
     // The scores of a step go where P of two steps before was.  The tensor core keeps the order of
-    // MMAs of one shape and accumulator only, so that step's P V must be waited for.  pv_done is
-    // waited for once per step, in order: a barrier two phases ahead would look incomplete.
+    // MMAs of one shape and accumulator only, so that step's P V must be waited for: v_empty tells
+    // that P V of both row tiles is over (every commit costs some 100 cycles, so there is one).
     for (long long x = x0; x < x1 && ok; ++local) {
       const int it = int(x / deal.nt), j0 = int(x - (long long)(it)*deal.nt);
       const int j1 = int(min((long long)(deal.nt), j0 + (x1 - x)));
@@ -249,17 +249,18 @@ __global__ void __launch_bounds__(608)
       for (int j = j0; j < j1; ++j, ++kv) {
         const int st = kv % C::NSTAGE;
         const int i = kv + 1, st2 = i % C::NSTAGE;
-        const uint32_t pk = (i / C::NSTAGE) & 1, pd = (kv - 1) & 1;
+        // step kv - 1
+        uint64_t* const last_pv = &bars->v_empty[(i + C::NSTAGE - 2) % C::NSTAGE];
+        const uint32_t pk = (i / C::NSTAGE) & 1, pd = kv > 0 ? ((kv - 1) / C::NSTAGE) & 1 : 1;
         if (j + 1 < j1) {
-          ok = kv > 0 ? warp_wait_all({&bars->k_full[st2], &bars->pv_done[0], &bars->pv_done[1]}, {pk, pd, pd}, p.wait_ns,
-                                      abort_flag, 324)
-                      : warp_wait(&bars->k_full[st2], pk, p.wait_ns, abort_flag, 324);
+          // (before the first step that barrier is in its first phase, whose predecessor counts as over)
+          ok = warp_wait_all({&bars->k_full[st2], last_pv}, {pk, pd}, p.wait_ns, abort_flag, 324);
           if (!ok) break;
           tc_fence_after();
           issue_S(i, i);
           if (j + 2 == j1) mma_commit_p(&bars->q_empty, leader);  // the item's last scores
-        } else if (kv > 0) {
-          if (!(ok = warp_wait_all({&bars->pv_done[0], &bars->pv_done[1]}, {pd, pd}, p.wait_ns, abort_flag, 325))) break;
+        } else if (!(ok = warp_wait(last_pv, pd, p.wait_ns, abort_flag, 326))) {
+          break;
         }
         const uint32_t pp = (kv >> 1) & 1;
         ok = warp_wait_all({&bars->v_full[st], &bars->p_full[0][kv & 1], &bars->p_full[1][kv & 1]},
@@ -275,10 +276,8 @@ __global__ void __launch_bounds__(608)
           __syncwarp();
         }
         tc_fence_after();
-        for (int t = 0; t < 2; ++t) {
-          issue_PV(t, st, kv, j == j0);
-          if (j + 1 == j1) mma_commit_p(&bars->o_final[t], leader);
-        }
+        issue_PV(0, st, kv, j == j0);
+        issue_PV(1, st, kv, j == j0);
         mma_commit_p(&bars->v_empty[st], leader);
       }
     }
@@ -350,9 +349,9 @@ __global__ void __launch_bounds__(608)
           const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
           l = l * alpha + (rsa.x + rsa.y);
           if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // u must hold the tile before this one, and no later one can have been added yet (this
-            // step's scores were issued after P V of two steps before, whose phase is over)
-            if (!(ok = warp_wait(&bars->pv_done[t], (g - 1) & 1, p.wait_ns, abort_flag, 332 + t))) break;
+            // u must hold the tile before this one, and no later one can have been added yet 
+            if (!(ok = warp_wait(&bars->v_empty[(g - 1) % C::NSTAGE], ((g - 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag,
+                                 332 + t))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -371,7 +370,8 @@ __global__ void __launch_bounds__(608)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[t][g & 1]);
       }
-      if (ok) ok = warp_wait(&bars->o_final[t], local & 1, p.wait_ns, abort_flag, 340 + t);
+      // P V of the item's last step
+      if (ok) ok = warp_wait(&bars->v_empty[(g - 1) % C::NSTAGE], ((g - 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag, 340 + t);
       if (!ok) break;
       if (idle) continue;
       tc_fence_after();
