@@ -30,6 +30,7 @@ backward); fp32 inputs (d = 64) on the CUDA cores.  Paged caches are
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -322,22 +323,34 @@ def _device(name, t, dim):
     return t.get_device()
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # (absent from a build of torch without CUDA)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(name, device, *args):
     """Run one entry point on the device of this index and its current stream."""
-    fn, packed = getattr(_lib, name), PACKED[name](*args)
-    if device == torch._C._cuda_getDevice():
-        st = fn(packed, torch._C._cuda_getCurrentRawStream(device))
+    fn, packed = getattr(_lib or lib(), name), PACKED[name](*args)
+    if device == _current_device():
+        st = fn(packed, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(packed, torch._C._cuda_getCurrentRawStream(device))
+            st = fn(packed, _raw_stream(device))
     if st:
         raise FAError(name, st)
+
+
+@functools.lru_cache(maxsize=1024)
+def _size(name, *args):
+    """A workspace size: it depends on its arguments alone."""
+    return int(getattr(lib(), name)(*args))
 
 
 def _workspace(workspace, need, like):
     """(address, bytes) of the caller's workspace, or of a new one; the last item keeps it alive."""
     if workspace is None:
-        workspace = like.new_empty(need or 1, dtype=torch.uint8)
+        if not need:
+            return 0, 0, None
+        workspace = like.new_empty(need, dtype=torch.uint8)
         return workspace.data_ptr(), need, workspace
     if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}, got {_described(workspace)}")
@@ -439,7 +452,6 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections=None, i
         k_out = k.new_empty(kshape)
     qo = _expect("q_out", q_out, shape, dtype, device)
     ko = _expect("k_out", k_out, kshape, dtype, device)
-    lib()
     _call("fa_qk_norm_rope", device, qp, kp, wq, wk, pos, freq, qo, ko, *qs, *ks, sa, sb, B, Hq, Hkv, N, d, rd, *sec,
           axes, 1 if interleaved else 0, eps, _DT[dtype])
     return q_out, k_out
@@ -475,11 +487,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_fr
     dkp, dks = _rows("dk", dk, grad_dtype, device, kshape)
     dwq = dwk = keep = None
     dwqp = dwkp = ws = ws_bytes = 0
-    L = lib()
     if wq:
         dwq, dwk = q.new_empty(d, dtype=torch.float32), q.new_empty(d, dtype=torch.float32)
         dwqp, dwkp = dwq.data_ptr(), dwk.data_ptr()
-        ws, ws_bytes, keep = _workspace(workspace, L.fa_qk_norm_rope_bwd_workspace_size(d), q)
+        ws, ws_bytes, keep = _workspace(workspace, _size("fa_qk_norm_rope_bwd_workspace_size", d), q)
     _call("fa_qk_norm_rope_bwd", device, dqo, dko, qp, kp, wq, wk, pos, freq, dqp, dkp, dwqp, dwkp, ws, ws_bytes, *qs,
           *ks, *dqs, *dks, sa, sb, B, Hq, Hkv, N, d, rd, *sec, axes, 1 if interleaved else 0, eps, _DT[dtype],
           _DT[dout_dtype], _DT[grad_dtype])
@@ -506,7 +517,6 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_cach
     if q_out is None:
         q_out = q.new_empty(shape)
     qo = _expect("q_out", q_out, shape, bf16, device)
-    lib()
     _call("fa_qk_norm_rope_append", device, qp, kp, vp, wq, wk, pos, freq, kc, vc, bt, ctx, ql, qo, *qs, *ks, *vs, sa, sb,
           R, Hq, Hkv, N, d, bs, maxb, num_blocks, rd, *sec, axes, 1 if interleaved else 0, eps, FA_DTYPE_BF16)
     return q_out
@@ -529,8 +539,7 @@ def _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device):
 
 
 def paged_decode_shared_workspace_size(R, Hq, Hkv, d, max_prefix_blocks, max_blocks_per_seq, block_size) -> int:
-    return int(lib().fa_paged_decode_shared_workspace_size(R, Hq, Hkv, d, max_prefix_blocks, max_blocks_per_seq,
-                                                           block_size))
+    return _size("fa_paged_decode_shared_workspace_size", R, Hq, Hkv, d, max_prefix_blocks, max_blocks_per_seq, block_size)
 
 
 def _decode_outputs(q, shape, device, with_lse, out):
@@ -556,8 +565,7 @@ def paged_decode_shared(q, k_cache, v_cache, prefix_table, prefix_len, block_tab
     pb = prefix_table.shape[0] if isinstance(prefix_table, torch.Tensor) and prefix_table.dim() == 1 else 0
     pt = _expect("prefix_table", prefix_table, (pb,), i32, device)
     pl = _expect("prefix_len", prefix_len, (1,), i32, device)
-    L = lib()
-    need = L.fa_paged_decode_shared_workspace_size(R, Hq, Hkv, d, pb, maxb, bs)
+    need = _size("fa_paged_decode_shared_workspace_size", R, Hq, Hkv, d, pb, maxb, bs)
     ws, ws_bytes, keep = _workspace(workspace, need, q)
     o, lse, op, lp = _decode_outputs(q, shape, device, with_lse, out)
     _call("fa_paged_decode_shared", device, qp, kc, vc, pt, pl, bt, ctx, op, lp, ws, ws_bytes, R, Hq, Hkv, d, bs, pb,
@@ -566,7 +574,7 @@ def paged_decode_shared(q, k_cache, v_cache, prefix_table, prefix_len, block_tab
 
 
 def paged_decode_scored_workspace_size(R, Hq, Hkv, d, max_blocks_per_seq, block_size) -> int:
-    return int(lib().fa_paged_decode_scored_workspace_size(R, Hq, Hkv, d, max_blocks_per_seq, block_size))
+    return _size("fa_paged_decode_scored_workspace_size", R, Hq, Hkv, d, max_blocks_per_seq, block_size)
 
 
 def paged_decode_scored(q, k_cache, v_cache, block_table, ctx_lens, weights, scale: float | None = None,
@@ -579,8 +587,7 @@ def paged_decode_scored(q, k_cache, v_cache, block_table, ctx_lens, weights, sca
     qp = _expect("q", q, shape, torch.bfloat16, device)
     num_blocks, bs, maxb, kc, vc, bt, ctx = _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device)
     w = _expect("weights", weights, (R, Hkv, maxb * bs), torch.float32, device)
-    L = lib()
-    need = L.fa_paged_decode_scored_workspace_size(R, Hq, Hkv, d, maxb, bs)
+    need = _size("fa_paged_decode_scored_workspace_size", R, Hq, Hkv, d, maxb, bs)
     ws, ws_bytes, keep = _workspace(workspace, need, q)
     o, lse, op, lp = _decode_outputs(q, shape, device, with_lse, out)
     _call("fa_paged_decode_scored", device, qp, kc, vc, bt, ctx, w, op, lp, ws, ws_bytes, R, Hq, Hkv, d, bs, maxb,
@@ -589,7 +596,7 @@ def paged_decode_scored(q, k_cache, v_cache, block_table, ctx_lens, weights, sca
 
 
 def paged_evict_workspace_size(R, Hkv, max_blocks_per_seq, keep) -> int:
-    return int(lib().fa_paged_evict_workspace_size(R, Hkv, max_blocks_per_seq, keep))
+    return _size("fa_paged_evict_workspace_size", R, Hkv, max_blocks_per_seq, keep)
 
 
 def paged_evict(k_cache, v_cache, block_table, ctx_lens, seq_lens, weights, slot_pos, keep: int, recent: int,
@@ -615,8 +622,8 @@ def paged_evict(k_cache, v_cache, block_table, ctx_lens, seq_lens, weights, slot
     wo = _expect("weights_out", weights_out, shape, f32, device)
     so = _expect("slot_pos_out", slot_pos_out, shape, i32, device)
     nc = _expect("new_ctx", new_ctx, (R,), i32, device)
-    L = lib()
-    ws, ws_bytes, alive = _workspace(workspace, L.fa_paged_evict_workspace_size(R, Hkv, maxb, keep), k_cache)
+    need = _size("fa_paged_evict_workspace_size", R, Hkv, maxb, keep)
+    ws, ws_bytes, alive = _workspace(workspace, need, k_cache)
     _call("fa_paged_evict", device, kc, vc, bt, ctx, seq, w, sp, wo, so, nc, ws, ws_bytes, R, Hkv, d, bs, maxb, num_blocks,
           keep, recent, FA_DTYPE_BF16)
     return new_ctx, weights_out, slot_pos_out

@@ -411,16 +411,20 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
   __shared__ float s_lse[ROWS];
   __shared__ float4 s_u[8][D / 4];
   const int G = p.Hq / p.Hkv, warp = warp_id(), lane = lane_id();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Lengths and old weights are read before the grid before this one is waited for: it let this one
+  // start after it had itself waited for everything before, and writes neither.
   if (int(blockIdx.x) < joins) {
     const int row = blockIdx.x * (8 / strands) + warp / strands, strand = warp % strands;
     const bool on = row < p.R * p.Hq;
+    const int n = on ? p.ctx[row / p.Hq] : 0;
+    const PartPieces x(p, on ? row / p.Hq : 0, on ? row % p.Hq / G : 0, n);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int Q = D / 4, PER = 32 / Q;  // lanes of a row, pieces a warp reads at a time
     float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
     float lse = 0.f;
     if (on) {
       const int r = row / p.Hq, h = row - r * p.Hq, g = h / G;
-      const PartPieces x(p, r, g, p.ctx[r]);
       const size_t row0 = size_t(r) * p.Hq + g * G;
       lse = part_lse_of(p, x, row0, h - g * G, s_w[warp]);
       const int pieces = x.np + x.no, c = (lane % Q) * 4;
@@ -465,18 +469,26 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
     const int at = blockIdx.x - joins, set = at / spans, span = at - set * spans;
     const int r = set / p.Hkv, g = set - r * p.Hkv;
     const int n = p.ctx[r];
-    if (span * JOIN_TOKENS >= n) return;
     const PartPieces x(p, r, g, n);
-    if (x.no == 0) return;  // a length out of range
+    const bool any = x.no > 0 && span * JOIN_TOKENS < n;  // (no pieces: a length out of range)
     const size_t row0 = size_t(r) * p.Hq + g * G, M = size_t(p.max_blocks) * BS;
+    float* const w0 = p.weights + (size_t(r) * p.Hkv + g) * M;
+    int s = span * JOIN_TOKENS + threadIdx.x * 4;
+    float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (any && s < n) old = *reinterpret_cast<const float4*>(w0 + s);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!any) return;
     for (int h = warp; h < G; h += 8) {
       const float lse = part_lse_of(p, x, row0, h, s_w[warp]);
       if (lane == 0) s_lse[h] = lse;
     }
     __syncthreads();
-    for (int s = span * JOIN_TOKENS + threadIdx.x * 4; s < n; s += spans * JOIN_TOKENS) {
-      float* out = p.weights + (size_t(r) * p.Hkv + g) * M + s;
-      const float4 old = *reinterpret_cast<const float4*>(out);
+    for (; s < n; s += spans * JOIN_TOKENS) {
+      float* out = w0 + s;
+      const int next = s + spans * JOIN_TOKENS;
+      const float4 cur = old;
+      if (next < n) old = *reinterpret_cast<const float4*>(w0 + next);
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int h = 0; h < G; ++h) {
@@ -488,11 +500,11 @@ __global__ void __launch_bounds__(256) fa_decode_join_kernel(const __grid_consta
         w.w += ex2(v.w - lse);
       }
       if (s + 4 <= n) {
-        *reinterpret_cast<float4*>(out) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+        *reinterpret_cast<float4*>(out) = make_float4(cur.x + w.x, cur.y + w.y, cur.z + w.z, cur.w + w.w);
       } else {
-        out[0] = old.x + w.x;
-        if (s + 1 < n) out[1] = old.y + w.y;
-        if (s + 2 < n) out[2] = old.z + w.z;
+        out[0] = cur.x + w.x;
+        if (s + 1 < n) out[1] = cur.y + w.y;
+        if (s + 2 < n) out[2] = cur.z + w.z;
       }
     }
   }

@@ -40,7 +40,7 @@ struct EvictParams {
   int* slot_pos_out;
   int* new_ctx;    // [R]
   int* moves;      // [R * Hkv][2 * cap]: destinations, then sources, as cache rows (block * Hkv + h) * 16 + slot
-  int* n_moves;    // [R * Hkv]
+  int* n_moves;    // [R * Hkv] (both for the second kernel)
   uint32_t* masks; // [R * Hkv][2][ceil(M / 32)], past MAX_KEYS only
   uint4 *kc, *vc;
   int R, Hkv, max_blocks, num_blocks, keep, recent, cap;
@@ -119,6 +119,8 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   __shared__ int s_warp[THREADS / 32];
   __shared__ int s_found[2];  // the digit's bin, and how many of its tokens are still needed
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (the second kernel's CTAs, held ready on the SMs, left it 10 us slower)
+  if (p.fused) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int r = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = lane_id();
   const size_t rh = size_t(r) * p.Hkv + h;
   const int M = p.max_blocks * BS;
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   if (bad || n <= p.keep) {  // out of range: left as it is; nothing to evict: the positions are written down
     if (tid == 0) {
       if (bad) set_status(FA_ERR_INVALID_ARG, 400);
-      p.n_moves[rh] = 0;
+      if (!p.fused) p.n_moves[rh] = 0;
       if (h == 0) p.new_ctx[r] = n;
     }
     for (int s = tid; s < M; s += THREADS) {
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
     reinterpret_cast<int4*>(so)[i] = pos;
   }
   __syncthreads();
-  if (tid == 0) p.n_moves[rh] = moves;
+  if (tid == 0 && !p.fused) p.n_moves[rh] = moves;
 #pragma unroll 2
   for (int i = tid; i < moves; i += THREADS) {
     const int a = src[i], b = dst[i];

@@ -333,7 +333,7 @@ EvictPlan evict_plan(int R, int Hkv, int max_blocks, int keep) {
   // rows go to a second kernel, which spreads them evenly: 32 requests x 8 heads of 4097 to 8192
   // tokens, kept 2048, moved in 67 us, while 256 CTAs on 148 SMs took 75 us.
   n.fused = n.in_smem && n.cap <= 512;
-  n.off_moves = align256(size_t(sets) * sizeof(int));
+  n.off_moves = n.fused ? 0 : align256(size_t(sets) * sizeof(int));
   n.off_masks = n.off_moves + (n.fused ? 0 : align256(size_t(sets) * 2 * n.cap * sizeof(int)));
   n.bytes = n.off_masks + (n.in_smem ? 0 : align256(size_t(sets) * 2 * ((M + 31) / 32) * sizeof(uint32_t)));
   return n;
@@ -533,10 +533,9 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
     return FA_ERR_UNSUPPORTED;
   if (a.R > 65535 || a.Hkv > 65535 || int64_t(a.max_blocks_per_seq) * evict::BS > 0x7fffffff ||
       int64_t(a.num_blocks) * a.Hkv * evict::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  if (!a.workspace || a.workspace_bytes < fa_paged_evict_workspace_size(a.R, a.Hkv, a.max_blocks_per_seq, a.keep) ||
-      !aligned(a.workspace, 256))
-    return FA_ERR_WORKSPACE;
   const EvictPlan n = evict_plan(a.R, a.Hkv, a.max_blocks_per_seq, a.keep);
+  if (n.bytes > 0 && (!a.workspace || a.workspace_bytes < n.bytes || !aligned(a.workspace, 256)))
+    return FA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(a.workspace);
   const EvictParams prm{a.block_table, a.ctx_lens, a.seq_lens, a.weights, a.slot_pos, a.weights_out, a.slot_pos_out,
                         a.new_ctx, reinterpret_cast<int*>(ws + n.off_moves), reinterpret_cast<int*>(ws),

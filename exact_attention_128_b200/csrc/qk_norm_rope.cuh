@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB)
   const bool norm = p.w[0] != nullptr;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int phys = 0, at = 0;  // paged: cache block and position of the token
   if constexpr (PAGED) {
     if (on) {
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(rope::THREADS, FA_ROPE_BWD_MINB) fa_qk_norm_ro
   const Runs<D, SPREAD> runs(c < C::PAIRS ? c : 0, p.rd);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float2 w[8], sum[8];  // weights, and their gradients' sums
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = both(0.f);
@@ -503,7 +505,6 @@ __global__ void __launch_bounds__(rope::THREADS, FA_ROPE_BWD_MINB) fa_qk_norm_ro
       if (on) store_row(dx + (h0 + i) * dh, runs, g);
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!norm) return;
   // rows of a warp, then the warps
   float* s_sum = reinterpret_cast<float*>(rope_smem);  // [warps][D], over the slots

@@ -408,7 +408,7 @@ typedef struct {
 fa_status fa_paged_decode_scored(const fa_paged_decode_scored_args* args, void* stream);
 
 /* fa_paged_evict_workspace_size — bytes of device workspace fa_paged_evict needs for its lists of
- * moves.  Returns 0 for invalid sizes. */
+ * moves.  Returns 0 where it needs none (few rows can move), and for invalid sizes. */
 size_t fa_paged_evict_workspace_size(int R, int Hkv, int max_blocks_per_seq, int keep);
 
 /*

@@ -99,7 +99,8 @@ def test_scored_rejects_on_host(L, kw, code):
     [(dict(kc=None), BAD), (dict(sp=None), BAD), (dict(nc=None), BAD), (dict(keep=0), BAD), (dict(recent=-1), BAD),
      (dict(recent=9), BAD), (dict(R=0), BAD), (dict(w=FAKE + 2), BAD), (dict(vc=FAKE + 8), BAD), (dict(wo=FAKE), BAD),
      (dict(so=FAKE), BAD), (dict(nc=FAKE), BAD), (dict(d=80), UNS), (dict(bs=8), UNS), (dict(dtype=fa.FA_DTYPE_F32), UNS),
-     (dict(R=70000), UNS), (dict(maxb=1 << 28), UNS), (dict(ws=None), WS), (dict(ws_bytes=16), WS)])
+     (dict(R=70000), UNS), (dict(maxb=1 << 28), UNS), (dict(maxb=200, keep=1000, ws=None), WS),
+     (dict(maxb=200, keep=1000, ws_bytes=16), WS)])
 def test_evict_rejects_on_host(L, kw, code):
     assert call(L, "fa_paged_evict", EVICT, kw) == code
 
@@ -136,7 +137,9 @@ def test_workspace_sizes(L):
     assert L.fa_paged_decode_shared_workspace_size(8, 13, 2, 128, 1, 20, 16) == 0
     b = L.fa_paged_decode_scored_workspace_size(8, 12, 2, 128, 20, 16)
     assert b >= 8 * 12 * 20 * 16 * 4 and b % 256 == 0
-    assert L.fa_paged_evict_workspace_size(8, 2, 20, 100) > 0 and L.fa_paged_evict_workspace_size(8, 2, 20, 0) == 0
+    assert L.fa_paged_evict_workspace_size(8, 2, 200, 1000) > 8 * 2 * 1000 * 8  # two lists of up to 1000 rows
+    assert L.fa_paged_evict_workspace_size(8, 2, 20, 100) == 0  # few rows: none
+    assert L.fa_paged_evict_workspace_size(8, 2, 200, 0) == 0
 
 
 def test_binding_rejects_cpu_tensors():
