@@ -60,6 +60,12 @@ fa_status rope_check(const int* positions, const double* inv_freq, int B, int Hq
   return FA_OK;
 }
 
+// Both weights, or neither.
+bool rope_weights(const void* q, const void* k, int dtype) {
+  const size_t size = dtype == FA_DTYPE_F32 ? 4 : 2;
+  return !q == !k && aligned(q, size) && aligned(k, size);
+}
+
 // Rows of 16-byte pieces at any (batch, head, token): base and strides (elements) are multiples of 16 bytes.
 bool rope_rows(const void* p, const int64_t* strides, int dtype) {
   const int64_t per = dtype == FA_DTYPE_F32 ? 4 : 8;
@@ -352,7 +358,7 @@ fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* args, void* stream) {
   if (s != FA_OK) return s;
   if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype)) return FA_ERR_INVALID_ARG;
   if (!a.q_out || !a.k_out || !aligned(a.q_out, 16) || !aligned(a.k_out, 16)) return FA_ERR_INVALID_ARG;
-  if (!a.q_weight != !a.k_weight || !aligned(a.q_weight, 2) || !aligned(a.k_weight, 2)) return FA_ERR_INVALID_ARG;
+  if (!rope_weights(a.q_weight, a.k_weight, a.dtype)) return FA_ERR_INVALID_ARG;
   RopeParams prm{{a.q, a.k, nullptr},
                  {a.q_strides[0], a.k_strides[0], 0},
                  {a.q_strides[1], a.k_strides[1], 0},
@@ -385,7 +391,7 @@ fa_status fa_qk_norm_rope_append(const fa_qk_norm_rope_append_args* args, void* 
   if (!aligned(a.q_out, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.block_table, 4) ||
       !aligned(a.ctx_lens, 4) || !aligned(a.q_lens, 4))
     return FA_ERR_INVALID_ARG;
-  if (!a.q_weight != !a.k_weight || !aligned(a.q_weight, 2) || !aligned(a.k_weight, 2)) return FA_ERR_INVALID_ARG;
+  if (!rope_weights(a.q_weight, a.k_weight, a.dtype)) return FA_ERR_INVALID_ARG;
   RopeParams prm{{a.q, a.k, a.v},
                  {a.q_strides[0], a.k_strides[0], a.v_strides[0]},
                  {a.q_strides[1], a.k_strides[1], a.v_strides[1]},
@@ -416,7 +422,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream
                                  a.dtype);
   if (s != FA_OK) return s;
   if (!a.dq_out || !a.dk_out || !aligned(a.dq_out, 16) || !aligned(a.dk_out, 16)) return FA_ERR_INVALID_ARG;
-  if (!a.q_weight != !a.k_weight || !aligned(a.q_weight, 2) || !aligned(a.k_weight, 2)) return FA_ERR_INVALID_ARG;
+  if (!rope_weights(a.q_weight, a.k_weight, a.dtype)) return FA_ERR_INVALID_ARG;
   if (a.dout_dtype != FA_DTYPE_F32 && a.dout_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
   if (a.grad_dtype != FA_DTYPE_F32 && a.grad_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
   if (a.dtype == FA_DTYPE_F32 && (a.dout_dtype != FA_DTYPE_F32 || a.grad_dtype != FA_DTYPE_F32)) return

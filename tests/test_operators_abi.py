@@ -46,13 +46,15 @@ ROTARY = [
     (dict(pos=None), BAD), (dict(freq=None), BAD), (dict(freq=FAKE + 4), BAD),
     (dict(sections=(31, 0, 0)), BAD), (dict(n_axes=0), BAD), (dict(n_axes=4), BAD), (dict(n_axes=2, sections=(33, -1, 0)), BAD),
     (dict(eps=0.0), BAD), (dict(eps=float("nan")), BAD), (dict(interleaved=2), BAD), (dict(rotary_dim=128), BAD),
-    (dict(rotary_dim=0), BAD), (dict(wq=None), BAD), (dict(q_strides=(2048, 68, 512)), BAD),
+    (dict(rotary_dim=0), BAD), (dict(wq=None), BAD), (dict(wk=FAKE + 1), BAD),
+    (dict(q_strides=(2048, 68, 512)), BAD),
     (dict(k=FAKE + 2), BAD), (dict(Hq=0), BAD), (dict(d=80), UNS), (dict(dtype=3), UNS),
     (dict(rotary_dim=24, sections=(12, 0, 0)), UNS),
 ]
 
 
-@pytest.mark.parametrize("kw,code", ROTARY + [(dict(q=None), BAD), (dict(qo=None), BAD), (dict(ko=FAKE + 4), BAD)])
+@pytest.mark.parametrize("kw,code", ROTARY + [(dict(q=None), BAD), (dict(qo=None), BAD), (dict(ko=FAKE + 4), BAD),
+                                              (dict(wk=FAKE + 2, dtype=fa.FA_DTYPE_F32), BAD)])
 def test_rope_rejects_on_host(L, kw, code):
     assert call(L, "fa_qk_norm_rope", FWD, kw) == code
 

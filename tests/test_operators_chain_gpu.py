@@ -201,3 +201,114 @@ def test_shared_prefix_step_equals_the_copied_prefix():
     torch.cuda.synchronize()
     assert (o.float() - o2.float()).abs().max() <= 2e-2 and (lse - lse2).abs().max() <= 1e-4
     assert fa.device_status() == 0
+
+
+def shared_case(R=70, P=700, seed=90):
+    Hq, Hkv, d = 8, 2, 128
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randperm(60 + R * 3, generator=g).int()
+    kc, vc = (randn((60 + R * 3, Hkv, 16, d), seed + i, BF).cuda() for i in (0, 1))
+    q = randn((R, Hq, d), seed + 2, BF).cuda()
+    ctx = torch.randint(0, 49, (R,), generator=g).int().cuda()
+    return q, kc, vc, ids[:50].cuda(), torch.tensor([P]).int().cuda(), ids[60:].view(R, 3).contiguous().cuda(), ctx
+
+
+def test_shared_prefix_step_replays_with_other_lengths():
+    """Captured once (prefix on the tensor cores, the requests' own part beside it), replayed as lengths grow."""
+    case = shared_case()
+    q, kc, vc, pt, pl, table, ctx = case
+    o = torch.empty_like(q)
+    fa.paged_decode_shared(*case, out=o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, lse = fa.paged_decode_shared(*case, out=o)
+    for t, P in enumerate((0, 1, 63, 64, 65, 640, 800)):
+        pl.fill_(P)
+        ctx.copy_((ctx + 7 * t) % 49)
+        q.copy_(randn(q.shape, 95 + t, BF))
+        graph.replay()
+        got, got_lse = o.clone(), lse.clone()
+        ref, ref_lse = fa.paged_decode_shared(*case)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref) and torch.equal(got_lse, ref_lse), P
+    assert fa.device_status() == 0
+
+
+def test_calls_on_several_streams_at_once():
+    """The same calls, each with its own workspace, on four streams without any order between them."""
+    cases = [shared_case(R, P, 200 + R) for R, P in ((70, 700), (3, 333), (128, 64), (1, 800))]
+    ref = [fa.paged_decode_shared(*c) for c in cases]
+    weights = [torch.zeros(c[0].shape[0], 2, 48, device="cuda") for c in cases]
+    for c, w in zip(cases, weights):
+        fa.paged_decode_scored(c[0], c[1], c[2], c[5], c[6], w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    mine = [torch.zeros_like(w) for w in weights]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for k, (s, c) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(s):
+                got[k].append(fa.paged_decode_shared(*c))
+                if i == 5:
+                    fa.paged_decode_scored(c[0], c[1], c[2], c[5], c[6], mine[k])
+    torch.cuda.synchronize()
+    for k in range(len(cases)):
+        for o, lse in got[k]:
+            assert torch.equal(o, ref[k][0]) and torch.equal(lse, ref[k][1])
+        assert torch.equal(mine[k], weights[k])
+    assert fa.device_status() == 0
+
+
+def test_blocks_past_32_bit_offsets():
+    """A pool of more than 2^31 values: the same calls on its last blocks and on a small pool give the same bits."""
+    Hkv, d, maxb, R, keep = 8, 128, 12, 3, 60
+    big = 2**31 // (Hkv * 16 * d) + 200
+    small = R * maxb + 4
+    ids = torch.randperm(small, generator=torch.Generator().manual_seed(1)).int()
+    table, pre = ids[: R * maxb].view(R, maxb).contiguous().cuda(), ids[R * maxb :].cuda()
+    far = big - small
+    ks, vs = (randn((small, Hkv, 16, d), 2 + i, BF).cuda() for i in (0, 1))
+    kb, vb = (torch.empty((big, Hkv, 16, d), device="cuda", dtype=BF) for _ in range(2))
+    kb[far:], vb[far:] = ks, vs
+    ctx, seq = (torch.tensor(x, device="cuda", dtype=torch.int32) for x in ((190, 100, 61), (200, 100, 61)))
+    wq, wk = weights(d, 5)
+    proj = randn((R, 4, 3 * Hkv, d), 6, BF).cuda()
+    q, k, v = (t.transpose(1, 2) for t in proj.split([Hkv, Hkv, Hkv], 2))
+    pos, freq = torch.arange(4, device="cuda", dtype=torch.int32), fa.rope_frequencies(d)
+    lens = torch.tensor([4, 0, 2], device="cuda", dtype=torch.int32)
+    out = []
+    for kc, vc, add in ((ks, vs, 0), (kb, vb, far)):
+        tb, pt = table + add, pre + add
+        q2 = torch.zeros(R, Hkv, 4, d, device="cuda", dtype=BF)
+        fa.qk_norm_rope_append(q, k, v, wq, wk, pos, freq, kc, vc, tb, ctx, lens, q_out=q2)
+        w = torch.rand(R, Hkv, maxb * 16, generator=torch.Generator().manual_seed(3)).cuda()
+        qd = q2[:, :, 0].contiguous()
+        o, lse = fa.paged_decode_scored(qd, kc, vc, tb, ctx, w)
+        o2, lse2 = fa.paged_decode_shared(qd, kc, vc, pt, torch.tensor([50], device="cuda", dtype=torch.int32), tb, ctx)
+        many = qd.repeat(30, 1, 1)  # enough rows for the tensor-core prefix
+        o3, _ = fa.paged_decode_shared(many, kc, vc, pt, torch.tensor([50], device="cuda", dtype=torch.int32),
+                                       tb.repeat(30, 1), ctx.repeat(30))
+        n, w2, sp = fa.paged_evict(kc, vc, tb, ctx, seq, w, torch.full_like(w, -1, dtype=torch.int32), keep, 10)
+        out.append((q2, o, lse, o2, lse2, o3, w, n, w2, sp, kc[add : add + small].clone(), vc[add : add + small].clone()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    assert fa.device_status() == 0
+
+
+def test_workspace_given_and_reused():
+    """One workspace for many calls in a row, of the size that is asked for and larger."""
+    case = shared_case(40, 300)
+    q, kc, vc, pt, pl, table, ctx = case
+    R, Hq, d = q.shape
+    need = fa.paged_decode_shared_workspace_size(R, Hq, 2, d, pt.shape[0], table.shape[1], 16)
+    ref = fa.paged_decode_shared(*case)
+    for size in (need, need + 4096):
+        ws = torch.full((size,), 255, device="cuda", dtype=torch.uint8)  # NaN everywhere
+        for _ in range(3):
+            o, lse = fa.paged_decode_shared(*case, workspace=ws)
+            assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    with pytest.raises(fa.FAError):
+        fa.paged_decode_shared(*case, workspace=torch.empty(need - 1, device="cuda", dtype=torch.uint8))
+    assert fa.device_status() == 0
