@@ -2,12 +2,6 @@
 // position rotation, the decode steps over pieces of the cache, and the eviction.  Included by
 // fa_api.cu, whose helpers (alignment, TMA descriptors, launches) it uses.
 #pragma once
-#ifndef FA_PART_PERSM
-#define FA_PART_PERSM 12
-#endif
-#ifndef FA_PREFIX_ROWS
-#define FA_PREFIX_ROWS 64
-#endif
 
 namespace {
 
@@ -89,7 +83,7 @@ fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
   const int64_t grid = (tgroups + prm.groups - 1) / prm.groups;
   if (tokens > 0x7fffff00 || grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
   auto kern = inter ? fa_qk_norm_rope_kernel<T, D, true, PAGED> : fa_qk_norm_rope_kernel<T, D, false, PAGED>;
-  const int smem = (sizeof(T) == 4 ? FA_ROPE_STAGES_F32 : FA_ROPE_STAGES) * rope::Slot<T, sizeof(T) == 4>::BYTES +
+  const int smem = (sizeof(T) == 4 ? rope::FWD_STAGES_F32 : rope::FWD_STAGES) * rope::Slot<T, sizeof(T) == 4>::BYTES +
                    (prm.groups * rope::TABLE + 8 * rope::Cfg<D>::L) * 16;
   static Prepared prepared[2];
   if (prepared[inter].launch(kern, dim3(unsigned(grid)), dim3(rope::THREADS), smem, st, prm) != cudaSuccess)
@@ -173,18 +167,29 @@ fa_status rope_by_d(RopeParams& prm, int d, bool inter, cudaStream_t st) {
 
 // ---- decode over pieces
 
-// Blocks of a piece: enough pieces for a few CTAs on each of 148 SMs when `sets` sets of rows
-// walk `blocks` blocks each, at least part::MIN_CHUNK blocks a piece and at most MAX_PARTS pieces.
+// Blocks of a piece when `sets` sets of rows walk up to `blocks` blocks each: enough pieces for 12
+// CTAs on each SM, which holds 3 (tables are wider than most contexts; 64 requests of 512 to 8192
+// tokens, 2 kv heads: 6, 12 and 24 CTAs took 72, 67 and 69 us), at least MIN_CHUNK blocks a piece
+// and at most MAX_PARTS pieces.
 int part_chunk(int64_t sets, int64_t blocks) {
-  const int64_t want = std::max<int64_t>(1, (148 * FA_PART_PERSM + sets - 1) / sets);
+  const int64_t want = std::max<int64_t>(1, (kSms * 12 + sets - 1) / sets);
   const int64_t pieces = std::min<int64_t>(part::MAX_PARTS, want);
   const int64_t c = std::max<int64_t>(part::MIN_CHUNK, (blocks + pieces - 1) / pieces);
   return int((c + part::WARPS - 1) / part::WARPS * part::WARPS);
 }
 
-// Rows per kv head from which the prefix goes to the tensor-core kernel, whose CTAs work on 256
-// rows at a time; below, 16-row pieces read the prefix again for each 16 rows.
-constexpr int kPrefixTensorRows = FA_PREFIX_ROWS;
+// Whether the prefix goes to the tensor-core kernel, whose CTAs work on 256 rows at a time, or to
+// 16-row pieces, which read the prefix again for each 16 rows but need no kernel of their own and
+// keep P exact.  By the work, in (16 rows x block)s of the prefix's table; one step with 1 to 64 own
+// tokens, pieces against tensor cores:
+//   8 kv heads x 4, d = 128: 200 tokens, 128 rows 16.8 / 14.1 us; 2000 tokens, 64 rows 27.2 / 16.6 us,
+//     512 rows 77.6 / 32.5 us; 16384 tokens, 512 rows 249 / 55.6 us
+//   2 kv heads x 6, d = 128: 200 tokens, 384 rows 14.0 / 15.6 us, 768 rows 17.0 / 16.4 us
+//   8 kv heads x 4, d = 64: 200 tokens, 256 rows 12.4 / 16.3 us; 2000 tokens, 64 rows 15.0 / 13.8 us
+// Below 64 rows the two differ by less than the time it takes to call them up to some 2000 tokens.
+bool prefix_on_tensor_cores(int64_t rows, int64_t row_tiles, int Hkv, int d, int prefix_blocks) {
+  return rows >= 64 && row_tiles * Hkv * prefix_blocks >= (d == 64 ? 3000 : 640);
+}
 
 struct PartPlan {
   int chunk, prefix_chunk, own_parts, prefix_parts, row_tiles;
@@ -197,18 +202,19 @@ PartPlan part_plan(int R, int Hq, int Hkv, int d, int max_blocks, int prefix_blo
   const int G = Hq / Hkv;
   n.chunk = part_chunk(int64_t(R) * Hkv, max_blocks);
   n.own_parts = (max_blocks + n.chunk - 1) / n.chunk;
-  if (prefix_blocks > 0 && int64_t(R) * G >= kPrefixTensorRows && G <= part::ROWS) {
+  const int64_t rows = int64_t(R) * G, row_tiles = (rows + part::ROWS - 1) / part::ROWS;
+  if (prefix_blocks > 0 && G <= part::ROWS && prefix_on_tensor_cores(rows, row_tiles, Hkv, d, prefix_blocks)) {
     n.RT = 128 / G;
     n.pairs = (R + 2 * n.RT - 1) / (2 * n.RT);
     n.pre_parts = int((part::PREFIX_CTAS + int64_t(n.pairs) * Hkv - 1) / (int64_t(n.pairs) * Hkv)) + 1;
   } else if (prefix_blocks > 0) {
-    n.row_tiles = int((int64_t(R) * G + part::ROWS - 1) / part::ROWS);
+    n.row_tiles = int(row_tiles);
     n.prefix_chunk = part_chunk(int64_t(n.row_tiles) * Hkv, prefix_blocks);
     n.prefix_parts = (prefix_blocks + n.prefix_chunk - 1) / n.prefix_chunk;
   }
-  const size_t rows = size_t(R) * Hq * (n.own_parts + n.prefix_parts);
-  n.off_lse = align256(rows * d * sizeof(float));
-  n.off_scores = n.off_lse + align256(rows * sizeof(float));
+  const size_t results = size_t(R) * Hq * (n.own_parts + n.prefix_parts);
+  n.off_lse = align256(results * d * sizeof(float));
+  n.off_scores = n.off_lse + align256(results * sizeof(float));
   n.off_pre_o = n.off_scores + (scored ? align256(size_t(R) * Hq * max_blocks * part::BS * sizeof(float)) : 0);
   const size_t pre_rows = size_t(n.pairs) * Hkv * n.pre_parts * 256;
   n.off_pre_lse = n.off_pre_o + pre_rows * d * sizeof(float);
@@ -305,7 +311,6 @@ fa_status part_call(const void* q, const void* k_cache, const void* v_cache, con
                     float* lse, int R, int Hq, int Hkv, int d, int max_prefix_blocks, int max_blocks, int num_blocks,
                     float scale, void* workspace, size_t workspace_bytes, void* stream) {
   const PartPlan n = part_plan(R, Hq, Hkv, d, max_blocks, max_prefix_blocks, weights != nullptr);
-  if (n.row_tiles > 65535) return FA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < n.bytes || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   PartParams prm{static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(o), lse,

@@ -15,7 +15,8 @@
 // and sine per token group, while the first rows are on their way; all heads' rows share them,
 // from shared memory, as they share the weights.  (With the angles of a lane's 8 pairs computed by
 // each warp for itself and kept in registers, 116 registers left 16 warps on an SM, and the
-// 8192-token prefill of 4 x 40 heads took 115 us instead of @@.)  A warp writes 1 KB of
+// 8192-token prefill of 4 x 40 heads took 115 us instead of 111, the fp32 image layer 33 instead of
+// 29.)  A warp writes 1 KB of
 // consecutive tokens of one head.
 //
 // Angles: the position (up to 2^31) times the frequency is taken in turns in 64 bits and reduced
@@ -25,25 +26,15 @@
 #include "common.cuh"
 
 namespace fa {
-#ifndef FA_ROPE_STAGES
-#define FA_ROPE_STAGES 5
-#endif
-#ifndef FA_ROPE_STAGES_F32
-#define FA_ROPE_STAGES_F32 4
-#endif
-#ifndef FA_ROPE_MINB
-#define FA_ROPE_MINB 3
-#endif
-#ifndef FA_ROPE_BWD_STAGES
-#define FA_ROPE_BWD_STAGES 4
-#endif
-#ifndef FA_ROPE_BWD_MINB
-#define FA_ROPE_BWD_MINB 2
-#endif
 namespace rope {
 constexpr int THREADS = 256;
 constexpr int MAX_CHUNK = 16;  // backward: heads of a unit, at most
-constexpr int BWD_STAGES = FA_ROPE_BWD_STAGES;  // backward: rows a thread has in flight, + 1
+// Rows a thread has in flight, + 1.  Forward: 3 CTAs on an SM; more stages or a fourth CTA at 64
+// registers were slower (prefill of 4 x 8192: 111 us; 7 stages 115, 4 CTAs 130).  Backward: 2 CTAs
+// of 128 registers; the forward's form, with angles and weights read from shared memory, took 99 us
+// on the training step (2 CTAs; 3 CTAs 142 to 149), this one 93.
+constexpr int FWD_STAGES = 5, FWD_STAGES_F32 = 4, FWD_CTAS = 3;
+constexpr int BWD_STAGES = 4, BWD_CTAS = 2;
 
 // Lanes of one row: d / 16 rounded up to a power of two (d = 96: 6 of 8 lanes work).
 template <int D>
@@ -299,12 +290,12 @@ __device__ __forceinline__ float row_sum(float v) {
 // PAGED (bf16): token (r, i) of request r is one of its last q_lens[r] positions; q' goes to
 // [R, Hq, N, d], k' and v to cache position ctx_lens[r] - q_lens[r] + i; padding rows are left.
 template <typename T, int D, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB)
+__global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
     fa_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   using namespace rope;
   using C = Cfg<D>;
   constexpr bool SPREAD = sizeof(T) == 4;
-  constexpr int STAGES = SPREAD ? FA_ROPE_STAGES_F32 : FA_ROPE_STAGES;
+  constexpr int STAGES = SPREAD ? FWD_STAGES_F32 : FWD_STAGES;
   using R = Slot<T, SPREAD>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
   float4* s_table = reinterpret_cast<float4*>(rope_smem + STAGES * R::BYTES);  // [groups][TABLE]
@@ -420,7 +411,8 @@ __global__ void __launch_bounds__(rope::THREADS, FA_ROPE_MINB)
 // to `part`, which the second kernel adds up in a fixed order (no atomics: the same call gives
 // the same bits).
 template <typename T, typename TG, typename TO, int D, bool INTER>
-__global__ void __launch_bounds__(rope::THREADS, FA_ROPE_BWD_MINB) fa_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
+__global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
+    fa_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
   using namespace rope;
   using C = Cfg<D>;
   constexpr bool SPREAD = sizeof(T) + sizeof(TG) + sizeof(TO) > 6;  // any of them fp32

@@ -278,6 +278,7 @@ def decode_case(lens, Hq, Hkv, d, maxb, seed, prefix=0):
     return q, kc, vc, table, ptable, torch.tensor(lens, dtype=torch.int32)
 
 
+@pytest.mark.parametrize("wide", [0, 800])  # a much wider prefix table sends 64 rows and more to the tensor cores
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize(
     "Hq,Hkv,prefix,lens",
@@ -298,8 +299,9 @@ def decode_case(lens, Hq, Hkv, d, maxb, seed, prefix=0):
         (4, 1, 16, (2,) * 16),
     ],
 )
-def test_decode_shared(d, Hq, Hkv, prefix, lens):
+def test_decode_shared(d, Hq, Hkv, prefix, lens, wide):
     q, kc, vc, table, ptable, ctx = decode_case(lens, Hq, Hkv, d, 40, 600 + d + prefix, prefix)
+    ptable = torch.cat([ptable, torch.full((wide,), -1, dtype=torch.int32)])
     dev = [t.cuda() for t in (q, kc, vc, ptable, torch.tensor([prefix], dtype=torch.int32), table, ctx)]
     o, lse = fa.paged_decode_shared(*dev)
     clean()
