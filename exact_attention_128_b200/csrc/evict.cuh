@@ -13,13 +13,16 @@
 // MAX_KEYS tokens).  The keep-th largest key is found in three digits of 9, 11 and 12 bits, from a
 // histogram each.  The first digit is a weight's exponent, of which few differ: its histogram has
 // 16 copies, one for every other lane, so that the lanes of a warp seldom add to one address (with
-// one copy of an 11-bit digit the selection of 8192 tokens took 32 us, most of it there).  Which tokens are above it, and which equal it, become bit masks of 32 tokens;
-// prefix sums of their population counts give every freed slot and every moving token its number.
+// one copy of an 11-bit digit the selection of 8192 tokens took 32 us, most of it there).  Which
+// tokens are above the threshold, and which equal it, become bit masks of 32 tokens; prefix sums of
+// their population counts give every freed slot and every moving token its number.
 // The CTA then moves the rows itself, or, where there are too few CTAs for the moves to fill the
 // device, a second kernel does.
 //
-// What bounds it: long prompts, the rows that move; steady eviction of few tokens, the latency of
-// the selection's passes over shared memory.
+// What bounds it: after long prompts, the rows that move (32 requests x 8 heads of 4097 to 8192 tokens,
+// keep 2048: 23 us of selection, then 66 us for about 390 MB of rows read and written, 5.9 TB/s); in
+// steady eviction of up to 128 tokens of 2176 (64 x 2 heads: 10 us), the selection's latency: two
+// passes over the weights, five over shared memory, a dozen barriers.
 #pragma once
 #include "common.cuh"
 
@@ -57,7 +60,7 @@ __device__ __forceinline__ uint32_t evict_key(float w) {
 }
 
 // Exclusive prefix sum of v over the CTA, and the total.
-__device__ __forceinline__ int evict_scan(int v, int* s_warp, int& total) {
+__device__ __forceinline__ int evict_scan(int v, int4* s_warp, int& total) {
   const int lane = lane_id(), warp = warp_id();
   int x = v;
 #pragma unroll
@@ -66,14 +69,14 @@ __device__ __forceinline__ int evict_scan(int v, int* s_warp, int& total) {
     if (lane >= d) x += y;
   }
   __syncthreads();  // the last call's readers are done
-  if (lane == 31) s_warp[warp] = x;
+  if (lane == 31) reinterpret_cast<int*>(s_warp)[warp] = x;
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < evict::THREADS / 32; ++w) {
-    const int t = s_warp[w];
-    before += w < warp ? t : 0;
-    all += t;
+  for (int w = 0; w < evict::THREADS / 32; w += 4) {
+    const int4 t = s_warp[w / 4];
+    before += (w < warp ? t.x : 0) + (w + 1 < warp ? t.y : 0) + (w + 2 < warp ? t.z : 0) + (w + 3 < warp ? t.w : 0);
+    all += t.x + t.y + t.z + t.w;
   }
   total = all;
   return before + x - v;
@@ -115,8 +118,8 @@ __device__ __forceinline__ void evict_move_rows(const EvictParams& p, const int*
 __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const __grid_constant__ EvictParams p) {
   using namespace evict;
   extern __shared__ uint32_t evict_smem[];
-  __shared__ int s_hist[BINS];
-  __shared__ int s_warp[THREADS / 32];
+  __shared__ __align__(16) int s_hist[BINS];
+  __shared__ int4 s_warp[THREADS / 128];
   __shared__ int s_found[2];  // the digit's bin, and how many of its tokens are still needed
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (the second kernel's CTAs, held ready on the SMs, left it 10 us slower)
@@ -155,17 +158,25 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   uint32_t* equal = above + MW;                                           // [words]: key at it; then the words' numbers
   const float4* w4 = reinterpret_cast<const float4*>(w);
   const int4* sp4 = reinterpret_cast<const int4*>(sp);
-  for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
+  for (int i = tid; i < BINS / 4; i += THREADS) reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  auto count_first = [&](int s, uint32_t k) {
+    if (s < n) atomicAdd(&s_hist[int(k >> 23) * COPIES + (lane & (COPIES - 1))], 1);
+  };
   if (p.in_smem) {
-#pragma unroll 2
+#pragma unroll 4
     for (int i = tid; 4 * i < n; i += THREADS) {  // (keys past n are not used)
       const float4 a = __ldg(w4 + i);
       const int4 v = __ldg(sp4 + i);
-      reinterpret_cast<uint4*>(s_key)[i] = make_uint4(key_from(4 * i, a.x, v.x), key_from(4 * i + 1, a.y, v.y),
-                                                      key_from(4 * i + 2, a.z, v.z), key_from(4 * i + 3, a.w, v.w));
+      const uint4 k = make_uint4(key_from(4 * i, a.x, v.x), key_from(4 * i + 1, a.y, v.y),
+                                 key_from(4 * i + 2, a.z, v.z), key_from(4 * i + 3, a.w, v.w));
+      reinterpret_cast<uint4*>(s_key)[i] = k;
+      count_first(4 * i, k.x);
+      count_first(4 * i + 1, k.y);
+      count_first(4 * i + 2, k.z);
+      count_first(4 * i + 3, k.w);
     }
   }
-  __syncthreads();
   auto key_of = [&](int s) { return p.in_smem ? s_key[s] : key_from(s, __ldg(w + s), __ldg(sp + s)); };
 
   // the keep-th largest key, digit by digit; `need` of the tokens that have it are kept
@@ -175,11 +186,15 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 23 : pass == 1 ? 12 : 0;
     const int bins = pass == 0 ? 512 : pass == 1 ? 2048 : 4096;
-    const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 23 : 12);
-    for (int s = tid; s < n; s += THREADS) {
-      const uint32_t k = key_of(s);
-      const int bin = (k >> shift) & (bins - 1);
-      if ((k & mask) == thr) atomicAdd(&s_hist[pass == 0 ? bin * COPIES + (lane & (COPIES - 1)) : bin], 1);
+    if (pass > 0) {
+      const uint32_t mask = 0xffffffffu << (pass == 1 ? 23 : 12);
+#pragma unroll 4
+      for (int s = tid; s < n; s += THREADS) {
+        const uint32_t k = key_of(s);
+        if ((k & mask) == thr) atomicAdd(&s_hist[(k >> shift) & (bins - 1)], 1);
+      }
+    } else if (!p.in_smem) {
+      for (int s = tid; s < n; s += THREADS) count_first(s, key_of(s));
     }
     __syncthreads();
     // a few bins a thread, the highest first
@@ -190,7 +205,11 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
       c[i] = 0;
       if (pass == 0) {
 #pragma unroll
-        for (int j = 0; j < COPIES; ++j) c[i] += s_hist[(top - i) * COPIES + ((j + lane) & (COPIES - 1))];
+        for (int j = 0; j < COPIES / 4; ++j) {
+          const int at = (top - i) * (COPIES / 4) + ((j + lane) & (COPIES / 4 - 1));
+          const int4 t = reinterpret_cast<const int4*>(s_hist)[at];
+          c[i] += t.x + t.y + t.z + t.w;
+        }
       } else {
         c[i] = s_hist[top - i];
       }
@@ -208,7 +227,8 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
       }
     }
     if (pass < 2)
-      for (int i = tid; i < 4096; i += THREADS) s_hist[i] = 0;  // (every thread has read its bins: evict_scan)
+      for (int i = tid; i < 1024; i += THREADS)  // (every thread has read its bins: evict_scan)
+        reinterpret_cast<int4*>(s_hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     thr |= uint32_t(s_found[0]) << shift;
     need = s_found[1];
@@ -242,10 +262,11 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
     const uint32_t below = lo <= 0 ? 0u : lo >= 32 ? 0xffffffffu : (1u << lo) - 1;
     const uint32_t live = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1;
     const int holes = __popc(~kept & below & live), movers = __popc(kept & ~below);
-    const int hole = evict_scan(holes, s_warp, total) + hole_done;
-    hole_done += total;
-    const int mover = evict_scan(movers, s_warp, total) + mover_done;
-    mover_done += total;
+    // (both sums of a round fit in 16 bits: 512 words of 32)
+    const int first = evict_scan(holes | movers << 16, s_warp, total);
+    const int hole = (first & 0xffff) + hole_done, mover = int(unsigned(first) >> 16) + mover_done;
+    hole_done += total & 0xffff;
+    mover_done += int(unsigned(total) >> 16);
     if (i < words) {
       above[i] = kept;
       equal[i] = uint32_t(lo > 0 ? hole : mover);  // (in the one word that may hold both, movers start at 0)
@@ -253,56 +274,77 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   }
   __syncthreads();
   const int moves = mover_done;  // == hole_done
-  // the lists take the keys' place once nothing reads a key (moves <= n / 2)
-  int* dst = p.in_smem && p.fused ? reinterpret_cast<int*>(s_key) : p.moves + rh * 2 * p.cap;
-  int* src = dst + (p.in_smem && p.fused ? M / 2 : p.cap);
-#pragma unroll 2
-  for (int i = tid; 4 * i < M; i += THREADS) {
-    float4 wt = make_float4(0.f, 0.f, 0.f, 0.f);
-    int4 pos = make_int4(-1, -1, -1, -1);
+  // The moving tokens in order, in the keys' place once nothing reads a key (moves <= n / 2), and
+  // the slots past keep emptied.
+  const bool in_place = p.in_smem && p.fused;
+  int* g_dst = p.moves + rh * 2 * p.cap;
+  int* src = p.in_smem ? reinterpret_cast<int*>(s_key) : g_dst + p.cap;
+  for (int i = p.keep / 4 + tid; 4 * i < M; i += THREADS) {
     if (4 * i < n) {
-      const float4 a = __ldg(w4 + i);
-      const int4 v = __ldg(sp4 + i);
-      const uint32_t kept = above[i >> 3], number = equal[i >> 3];
-      const int first = (4 * i) & ~31, lo = p.keep - first;
-      // movers of this word: its kept tokens past keep
+      const uint32_t kept = above[i >> 3];
+      const int lo = p.keep - ((4 * i) & ~31);
       const uint32_t past = kept & (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1));
+      const int number = lo > 0 ? 0 : int(equal[i >> 3]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int s = 4 * i + j;
-        const uint32_t bit = 1u << (s & 31);
-        if (s >= n) continue;
-        if (s >= p.keep) {
-          if (kept & bit) src[(lo > 0 ? 0 : int(number)) + __popc(past & (bit - 1))] = s;
-        } else if (kept & bit) {
-          (j == 0 ? wt.x : j == 1 ? wt.y : j == 2 ? wt.z : wt.w) = j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w;
-          (j == 0 ? pos.x : j == 1 ? pos.y : j == 2 ? pos.z : pos.w) =
-              pos_of(s, j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
-        } else {
-          dst[int(number) + __popc(~kept & (bit - 1))] = s;
-        }
+        const uint32_t bit = 1u << ((4 * i + j) & 31);
+        if (past & bit) src[number + __popc(past & (bit - 1))] = 4 * i + j;
       }
     }
-    reinterpret_cast<float4*>(wo)[i] = wt;
-    reinterpret_cast<int4*>(so)[i] = pos;
+    if (4 * i >= p.keep) {
+      reinterpret_cast<float4*>(wo)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      reinterpret_cast<int4*>(so)[i] = make_int4(-1, -1, -1, -1);
+    }
   }
   __syncthreads();
   if (tid == 0 && !p.fused) p.n_moves[rh] = moves;
+  // The slots below keep: their own token, or the moving token of the freed slot's number, whose
+  // weight and position are gathered here (scattered to the slots afterwards, 4 bytes of a sector
+  // each, the selection of 32 x 8 x 8192 tokens took 24.3 us; gathered, 23.1 us).
+  int* out_src = in_place ? src : g_dst + p.cap;
+  int* out_dst = in_place ? src + M / 2 : g_dst;
 #pragma unroll 2
-  for (int i = tid; i < moves; i += THREADS) {
-    const int a = src[i], b = dst[i];
-    wo[b] = __ldg(w + a);
-    so[b] = pos_of(a, __ldg(sp + a));
-    // from slots to cache rows
-    const int pa = __ldg(bt + a / BS), pb = __ldg(bt + b / BS);
-    const bool ok = pa >= 0 && pa < p.num_blocks && pb >= 0 && pb < p.num_blocks;
-    if (!ok) set_status(FA_ERR_INVALID_ARG, 401);
-    src[i] = ok ? (pa * p.Hkv + h) * BS + a % BS : -1;
-    dst[i] = ok ? (pb * p.Hkv + h) * BS + b % BS : -1;
+  for (int i = tid; 4 * i < p.keep; i += THREADS) {
+    const uint32_t kept = above[i >> 3];
+    const int number = int(equal[i >> 3]);
+    const float4 a = __ldg(w4 + i);
+    const int4 v = __ldg(sp4 + i);
+    float wt[4] = {a.x, a.y, a.z, a.w};
+    int pos[4] = {v.x, v.y, v.z, v.w}, from[4], page[4], to = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // the slot whose token comes here
+      const int s = 4 * i + j;
+      from[j] = s >= p.keep ? -1 : (kept >> (s & 31)) & 1 ? s : src[number + __popc(~kept & ((1u << (s & 31)) - 1))];
+    }
+    bool moved = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (from[j] < 0 || from[j] == 4 * i + j) continue;
+      moved = true;
+      wt[j] = __ldg(w + from[j]);
+      pos[j] = __ldg(sp + from[j]);
+      page[j] = __ldg(bt + from[j] / BS);
+    }
+    if (moved) to = __ldg(bt + i / (BS / 4));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int s = 4 * i + j;
+      if (from[j] >= 0 && from[j] != s) {
+        const bool ok = page[j] >= 0 && page[j] < p.num_blocks && to >= 0 && to < p.num_blocks;
+        if (!ok) set_status(FA_ERR_INVALID_ARG, 401);
+        const int at = number + __popc(~kept & ((1u << (s & 31)) - 1));
+        out_src[at] = ok ? (page[j] * p.Hkv + h) * BS + from[j] % BS : -1;
+        out_dst[at] = ok ? (to * p.Hkv + h) * BS + s % BS : -1;
+      }
+      wt[j] = from[j] >= 0 ? wt[j] : 0.f;
+      pos[j] = from[j] >= 0 ? pos_of(from[j], pos[j]) : -1;
+    }
+    reinterpret_cast<float4*>(wo)[i] = make_float4(wt[0], wt[1], wt[2], wt[3]);
+    reinterpret_cast<int4*>(so)[i] = make_int4(pos[0], pos[1], pos[2], pos[3]);
   }
   if (!p.fused) return;
   __syncthreads();
-  evict_move_rows(p, dst, src, moves, tid, THREADS);
+  evict_move_rows(p, out_dst, out_src, moves, tid, THREADS);
 }
 
 __global__ void __launch_bounds__(256) fa_evict_move_kernel(const __grid_constant__ EvictParams p) {

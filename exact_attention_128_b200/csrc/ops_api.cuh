@@ -6,8 +6,9 @@
 namespace {
 
 // A kernel whose launches need attributes (dynamic shared memory past 48 KB, the SM's memory as
-// shared memory): they are set at its first launch on each device, and again should a launch fail
-// (a reset device has forgotten them).
+// shared memory): they are set at its first launch on each device, and again should a launch need
+// more memory or fail (a reset device has forgotten them).  Never to less than before: threads may
+// launch at once.
 class Prepared {
  public:
   template <typename... KArgs, typename... Args>
@@ -15,20 +16,23 @@ class Prepared {
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     std::atomic<int>& have = smem_[dev & 63];
-    if (have.load(std::memory_order_relaxed) >= smem) {
+    if (have.load(std::memory_order_acquire) >= smem) {
       if (launch_pdl(kernel, grid, block, smem, st, args...) == cudaSuccess) return cudaSuccess;
       cudaGetLastError();
     }
-    if (cudaError_t e = set_smem(kernel, smem)) return e;
+    std::lock_guard<std::mutex> lock(setting_);
+    const int most = std::max(smem, have.load(std::memory_order_relaxed));
+    if (cudaError_t e = set_smem(kernel, most)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                              cudaSharedmemCarveoutMaxShared))
       return e;
-    have.store(smem, std::memory_order_relaxed);
+    have.store(most, std::memory_order_release);
     return launch_pdl(kernel, grid, block, smem, st, args...);
   }
 
  private:
-  std::atomic<int> smem_[64] = {};
+  std::atomic<int> smem_[64] = {};  // of each device; 0: not launched yet
+  std::mutex setting_;
 };
 
 constexpr int kSms = 148;  // SMs that work is divided for
@@ -136,8 +140,8 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
   constexpr int SMEM = rope::BWD_STAGES * rope::THREADS * 16 * int(sizeof(T) + sizeof(TG));
   static_assert(SMEM >= WARPS * D * 4, "the weight-gradient sums reuse the slots");
   static Prepared prepared[2];
-  if (prepared[inter].launch(kern, dim3(unsigned(ctas[0] + ctas[1])), dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess)
-    return FA_ERR_CUDA;
+  const dim3 grid(unsigned(ctas[0] + ctas[1]));
+  if (prepared[inter].launch(kern, grid, dim3(rope::THREADS), SMEM, st, prm) != cudaSuccess) return FA_ERR_CUDA;
   if (prm.w[0] && launch_pdl(fa_qk_norm_rope_dw_kernel, dim3(D / 8, 2), dim3(512), 0, st,
                              static_cast<const float*>(prm.part), dwq, dwk, D, ctas[0], ctas[0] + ctas[1]) !=
                                  cudaSuccess)
@@ -279,8 +283,9 @@ fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm
   const int64_t joins = (int64_t(prm.R) * prm.Hq * strands + 7) / 8;
   const int64_t sets = int64_t(prm.R) * prm.Hkv;
   // spans of weights: four CTAs for each SM in all, at most one per JOIN_TOKENS tokens
-  const int64_t spans = std::min<int64_t>((int64_t(prm.max_blocks) * part::BS + part::JOIN_TOKENS - 1) / part::JOIN_TOKENS,
-                                          std::max<int64_t>(1, 148 * 4 / sets));
+  const int64_t tokens = int64_t(prm.max_blocks) * part::BS;
+  const int64_t spans = std::min<int64_t>((tokens + part::JOIN_TOKENS - 1) / part::JOIN_TOKENS,
+                                          std::max<int64_t>(1, kSms * 4 / sets));
   const int64_t grid = joins + (scored ? sets * spans : 0);
   if (grid > 0x7fffffff) return FA_ERR_UNSUPPORTED;
   auto join = scored ? fa_decode_join_kernel<D, true> : fa_decode_join_kernel<D, false>;
@@ -290,9 +295,8 @@ fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm
 }
 
 fa_status part_check(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                     const int* ctx_lens, const void* o, const float* lse, int R, int Hq, int Hkv, int d, int
-                         block_size,
-                     int max_blocks, int num_blocks, float scale, int dtype) {
+                     const int* ctx_lens, const void* o, const float* lse, int R, int Hq, int Hkv, int d,
+                     int block_size, int max_blocks, int num_blocks, float scale, int dtype) {
   if (!q || !k_cache || !v_cache || !block_table || !ctx_lens || !o) return FA_ERR_INVALID_ARG;
   if (!part_sizes(R, Hq, Hkv, d, max_blocks, block_size) || num_blocks <= 0) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
@@ -316,8 +320,8 @@ fa_status part_call(const void* q, const void* k_cache, const void* v_cache, con
   PartParams prm{static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(o), lse,
                  reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + n.off_lse),
                  reinterpret_cast<float*>(ws + n.off_scores), weights, block_table, ctx_lens, prefix_table, prefix_len,
-                 R, Hq, Hkv, max_blocks, max_prefix_blocks, num_blocks, n.own_parts + n.prefix_parts, n.prefix_parts, n.own_parts, 0,
-                 n.chunk, n.prefix_chunk,
+                 R, Hq, Hkv, max_blocks, max_prefix_blocks, num_blocks, n.own_parts + n.prefix_parts,
+                 n.prefix_parts, n.own_parts, 0, n.chunk, n.prefix_chunk,
                  n.pairs > 0 ? reinterpret_cast<const float*>(ws + n.off_pre_o) : nullptr,
                  n.pairs > 0 ? reinterpret_cast<const float*>(ws + n.off_pre_lse) : nullptr,
                  n.pre_parts, n.pairs, n.RT, false, scale * 1.4426950408889634f, g_wait_ns};
@@ -358,8 +362,7 @@ fa_status fa_qk_norm_rope(const fa_qk_norm_rope_args* args, void* stream) {
   if (!args) return FA_ERR_INVALID_ARG;
   const fa_qk_norm_rope_args& a = *args;
   const fa_status s = rope_check(a.positions, a.inv_freq, a.B, a.Hq, a.Hkv, a.N, a.d, a.rotary_dim, a.sections,
-                                 a.n_axes, a.interleaved, a.eps,
-                                 a.dtype);
+                                 a.n_axes, a.interleaved, a.eps, a.dtype);
   if (s != FA_OK) return s;
   if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype)) return FA_ERR_INVALID_ARG;
   if (!a.q_out || !a.k_out || !aligned(a.q_out, 16) || !aligned(a.k_out, 16)) return FA_ERR_INVALID_ARG;
@@ -383,14 +386,13 @@ fa_status fa_qk_norm_rope_append(const fa_qk_norm_rope_append_args* args, void* 
   if (!args) return FA_ERR_INVALID_ARG;
   const fa_qk_norm_rope_append_args& a = *args;
   const fa_status s = rope_check(a.positions, a.inv_freq, a.R, a.Hq, a.Hkv, a.Nq_max, a.d, a.rotary_dim, a.sections,
-                                 a.n_axes, a.interleaved,
-                                 a.eps, a.dtype);
+                                 a.n_axes, a.interleaved, a.eps, a.dtype);
   if (s != FA_OK) return s;
   if (a.block_size <= 0 || a.max_blocks_per_seq <= 0 || a.num_blocks <= 0) return FA_ERR_INVALID_ARG;
   if (a.dtype != FA_DTYPE_BF16 || a.d == 256 || a.block_size != 16) return FA_ERR_UNSUPPORTED;
   if (int64_t(a.max_blocks_per_seq) * 16 > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) || !rope_rows(a.v, a.v_strides,
-      a.dtype))
+  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) ||
+      !rope_rows(a.v, a.v_strides, a.dtype))
     return FA_ERR_INVALID_ARG;
   if (!a.q_out || !a.k_cache || !a.v_cache || !a.block_table || !a.ctx_lens || !a.q_lens) return FA_ERR_INVALID_ARG;
   if (!aligned(a.q_out, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) || !aligned(a.block_table, 4) ||
@@ -423,18 +425,16 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream
   if (!args) return FA_ERR_INVALID_ARG;
   const fa_qk_norm_rope_bwd_args& a = *args;
   const fa_status s = rope_check(a.positions, a.inv_freq, a.B, a.Hq, a.Hkv, a.N, a.d, a.rotary_dim, a.sections,
-                                 a.n_axes, a.interleaved, a.eps,
-                                 a.dtype);
+                                 a.n_axes, a.interleaved, a.eps, a.dtype);
   if (s != FA_OK) return s;
   if (!a.dq_out || !a.dk_out || !aligned(a.dq_out, 16) || !aligned(a.dk_out, 16)) return FA_ERR_INVALID_ARG;
   if (!rope_weights(a.q_weight, a.k_weight, a.dtype)) return FA_ERR_INVALID_ARG;
   if (a.dout_dtype != FA_DTYPE_F32 && a.dout_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
   if (a.grad_dtype != FA_DTYPE_F32 && a.grad_dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
-  if (a.dtype == FA_DTYPE_F32 && (a.dout_dtype != FA_DTYPE_F32 || a.grad_dtype != FA_DTYPE_F32)) return
-      FA_ERR_UNSUPPORTED;
-  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) || !rope_rows(a.dq, a.dq_strides,
-      a.grad_dtype) ||
-      !rope_rows(a.dk, a.dk_strides, a.grad_dtype))
+  if (a.dtype == FA_DTYPE_F32 && (a.dout_dtype != FA_DTYPE_F32 || a.grad_dtype != FA_DTYPE_F32))
+    return FA_ERR_UNSUPPORTED;
+  if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) ||
+      !rope_rows(a.dq, a.dq_strides, a.grad_dtype) || !rope_rows(a.dk, a.dk_strides, a.grad_dtype))
     return FA_ERR_INVALID_ARG;
   // no two rows of a gradient may share memory
   const int n[2][3] = {{a.B, a.Hq, a.N}, {a.B, a.Hkv, a.N}};
@@ -461,17 +461,15 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream
                     a.pos_axis_stride, a.pos_batch_stride, a.B, {a.Hq, a.Hkv}, a.N, a.rotary_dim, a.sections[0],
                     a.n_axes > 1 ? a.sections[0] + a.sections[1] : a.sections[0], a.eps, {1, 1}, {1, 1}, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.dtype == FA_DTYPE_F32) return rope_bwd_by_d<float, float, float>(prm, a.d, a.interleaved, a.dq_weight,
-      a.dk_weight, st);
+  float *dwq = a.dq_weight, *dwk = a.dk_weight;
+  if (a.dtype == FA_DTYPE_F32) return rope_bwd_by_d<float, float, float>(prm, a.d, a.interleaved, dwq, dwk, st);
   using bf = __nv_bfloat16;
+  const bool out_f32 = a.grad_dtype == FA_DTYPE_F32;
   if (a.dout_dtype == FA_DTYPE_F32)
-    return a.grad_dtype == FA_DTYPE_F32 ? rope_bwd_by_d<bf, float, float>(prm, a.d, a.interleaved, a.dq_weight,
-        a.dk_weight, st)
-                                      : rope_bwd_by_d<bf, float, bf>(prm, a.d, a.interleaved, a.dq_weight, a.dk_weight,
-                                          st);
-  return a.grad_dtype == FA_DTYPE_F32 ? rope_bwd_by_d<bf, bf, float>(prm, a.d, a.interleaved, a.dq_weight, a.dk_weight,
-      st)
-                                    : rope_bwd_by_d<bf, bf, bf>(prm, a.d, a.interleaved, a.dq_weight, a.dk_weight, st);
+    return out_f32 ? rope_bwd_by_d<bf, float, float>(prm, a.d, a.interleaved, dwq, dwk, st)
+                   : rope_bwd_by_d<bf, float, bf>(prm, a.d, a.interleaved, dwq, dwk, st);
+  return out_f32 ? rope_bwd_by_d<bf, bf, float>(prm, a.d, a.interleaved, dwq, dwk, st)
+                 : rope_bwd_by_d<bf, bf, bf>(prm, a.d, a.interleaved, dwq, dwk, st);
 }
 
 size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int max_prefix_blocks,
@@ -487,14 +485,12 @@ fa_status fa_paged_decode_shared(const fa_paged_decode_shared_args* args, void* 
       !aligned(a.prefix_len, 4))
     return FA_ERR_INVALID_ARG;
   const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
-                                 a.d, a.block_size,
-                                 a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
+                                 a.d, a.block_size, a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
   if (s != FA_OK) return s;
   if (int64_t(a.max_prefix_blocks) * part::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
   return part_call(a.q, a.k_cache, a.v_cache, a.prefix_table, a.prefix_len, a.block_table, a.ctx_lens, nullptr, a.o,
-                   a.lse, a.R, a.Hq, a.Hkv, a.d,
-                   a.max_prefix_blocks, a.max_blocks_per_seq, a.num_blocks, a.scale, a.workspace, a.workspace_bytes,
-                       stream);
+                   a.lse, a.R, a.Hq, a.Hkv, a.d, a.max_prefix_blocks, a.max_blocks_per_seq, a.num_blocks, a.scale,
+                   a.workspace, a.workspace_bytes, stream);
 }
 
 size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int max_blocks_per_seq, int block_size) {
@@ -507,12 +503,11 @@ fa_status fa_paged_decode_scored(const fa_paged_decode_scored_args* args, void* 
   const fa_paged_decode_scored_args& a = *args;
   if (!a.weights || !aligned(a.weights, 16)) return FA_ERR_INVALID_ARG;
   const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
-                                 a.d, a.block_size,
-                                 a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
+                                 a.d, a.block_size, a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
   if (s != FA_OK) return s;
   return part_call(a.q, a.k_cache, a.v_cache, nullptr, nullptr, a.block_table, a.ctx_lens, a.weights, a.o, a.lse, a.R,
-                   a.Hq, a.Hkv, a.d, 0,
-                   a.max_blocks_per_seq, a.num_blocks, a.scale, a.workspace, a.workspace_bytes, stream);
+                   a.Hq, a.Hkv, a.d, 0, a.max_blocks_per_seq, a.num_blocks, a.scale, a.workspace, a.workspace_bytes,
+                   stream);
 }
 
 size_t fa_paged_evict_workspace_size(int R, int Hkv, int max_blocks_per_seq, int keep) {
@@ -524,14 +519,13 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
   if (!args) return FA_ERR_INVALID_ARG;
   const fa_paged_evict_args& a = *args;
   if (!a.k_cache || !a.v_cache || !a.block_table || !a.ctx_lens || !a.seq_lens || !a.weights || !a.slot_pos ||
-      !a.weights_out ||
-      !a.slot_pos_out || !a.new_ctx)
+      !a.weights_out || !a.slot_pos_out || !a.new_ctx)
     return FA_ERR_INVALID_ARG;
   if (a.R <= 0 || a.Hkv <= 0 || a.d <= 0 || a.block_size <= 0 || a.max_blocks_per_seq <= 0 || a.num_blocks <= 0)
     return FA_ERR_INVALID_ARG;
   if (a.keep <= 0 || a.recent < 0 || a.recent > a.keep) return FA_ERR_INVALID_ARG;
-  const void* small[] = {a.block_table, a.ctx_lens, a.seq_lens, a.weights, a.slot_pos, a.weights_out, a.slot_pos_out,
-      a.new_ctx};
+  const void* small[] = {a.block_table, a.ctx_lens, a.seq_lens, a.weights, a.slot_pos, a.weights_out,
+                         a.slot_pos_out, a.new_ctx};
   for (const void* p : small)
     if (!aligned(p, 4)) return FA_ERR_INVALID_ARG;
   const void* large[] = {a.k_cache, a.v_cache, a.weights, a.slot_pos, a.weights_out, a.slot_pos_out};
@@ -543,7 +537,8 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
   if (a.dtype != FA_DTYPE_BF16 || (a.d != 64 && a.d != 96 && a.d != 128 && a.d != 256) || a.block_size != evict::BS)
     return FA_ERR_UNSUPPORTED;
   if (a.R > 65535 || a.Hkv > 65535 || int64_t(a.max_blocks_per_seq) * evict::BS > 0x7fffffff ||
-      int64_t(a.num_blocks) * a.Hkv * evict::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+      int64_t(a.num_blocks) * a.Hkv * evict::BS > 0x7fffffff)
+    return FA_ERR_UNSUPPORTED;
   const EvictPlan n = evict_plan(a.R, a.Hkv, a.max_blocks_per_seq, a.keep);
   if (n.bytes > 0 && (!a.workspace || a.workspace_bytes < n.bytes || !aligned(a.workspace, 256)))
     return FA_ERR_WORKSPACE;
@@ -561,7 +556,7 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
     return FA_ERR_CUDA;
   if (!n.fused && n.cap > 0) {
     const int64_t pieces = int64_t(n.cap) * 2 * prm.row16;
-    const int64_t want = std::max<int64_t>(1, 148 * 16 / (int64_t(a.R) * a.Hkv));
+    const int64_t want = std::max<int64_t>(1, kSms * 16 / (int64_t(a.R) * a.Hkv));
     const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(want, (pieces + 1023) / 1024)));
     if (launch_pdl(fa_evict_move_kernel, dim3(grid, a.Hkv, a.R), dim3(256), 0, st, prm) != cudaSuccess)
       return FA_ERR_CUDA;
