@@ -329,7 +329,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _call(name, device, *args):
     """Run one entry point on the device of this index and its current stream."""
-    fn, packed = getattr(_lib or lib(), name), PACKED[name](*args)
+    fn = getattr(_lib or lib(), name)
+    try:
+        packed = PACKED[name](*args)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"{name}: a size or option is out of its C type's range: {e}") from None
     if device == _current_device():
         st = fn(packed, _raw_stream(device))
     else:
@@ -342,7 +346,10 @@ def _call(name, device, *args):
 @functools.lru_cache(maxsize=1024)
 def _size(name, *args):
     """A workspace size: it depends on its arguments alone."""
-    return int(getattr(lib(), name)(*args))
+    try:
+        return int(getattr(lib(), name)(*args))
+    except ctypes.ArgumentError as e:
+        raise ValueError(f"{name}: {e}") from None
 
 
 def _workspace(workspace, need, like):
@@ -422,14 +429,6 @@ def _heads(name, t):
     return t.shape[1]
 
 
-def _like_rows(t, B, H, N, d, dtype):
-    """An empty [B,H,N,d] tensor: as [B,N,H,d] in memory where t is a view of a projection, else contiguous."""
-    strides = t.stride()
-    if strides[2] > strides[1]:
-        return torch.empty_strided((B, H, N, d), (N * H * d, d, H * d, 1), dtype=dtype, device=t.device)
-    return t.new_empty((B, H, N, d), dtype=dtype)
-
-
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, sections=None, interleaved: bool = False,
                  eps: float = 1e-6, q_out=None, k_out=None):
     """Per-head RMS norm and rotation: q [B,Hq,N,d], k [B,Hkv,N,d] (views with contiguous rows, as
@@ -480,9 +479,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_fr
     pos, sa, sb, freq, rd, sec, axes = _rope_args(device, positions, inv_freq, sections, B, N)
     wq, wk = _rope_weights(q_weight, k_weight, d, dtype, device)
     if dq is None:
-        dq = _like_rows(q, B, Hq, N, d, grad_dtype)
+        dq = torch.empty_like(q, dtype=grad_dtype)  # (dense, its dimensions in the order of q's)
     if dk is None:
-        dk = _like_rows(k, B, Hkv, N, d, grad_dtype)
+        dk = torch.empty_like(k, dtype=grad_dtype)
     dqp, dqs = _rows("dq", dq, grad_dtype, device, shape)
     dkp, dks = _rows("dk", dk, grad_dtype, device, kshape)
     dwq = dwk = keep = None
@@ -517,8 +516,8 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_cach
     if q_out is None:
         q_out = q.new_empty(shape)
     qo = _expect("q_out", q_out, shape, bf16, device)
-    _call("fa_qk_norm_rope_append", device, qp, kp, vp, wq, wk, pos, freq, kc, vc, bt, ctx, ql, qo, *qs, *ks, *vs, sa, sb,
-          R, Hq, Hkv, N, d, bs, maxb, num_blocks, rd, *sec, axes, 1 if interleaved else 0, eps, FA_DTYPE_BF16)
+    _call("fa_qk_norm_rope_append", device, qp, kp, vp, wq, wk, pos, freq, kc, vc, bt, ctx, ql, qo, *qs, *ks, *vs, sa,
+          sb, R, Hq, Hkv, N, d, bs, maxb, num_blocks, rd, *sec, axes, 1 if interleaved else 0, eps, FA_DTYPE_BF16)
     return q_out
 
 
@@ -539,7 +538,8 @@ def _cache_args(k_cache, v_cache, block_table, ctx_lens, R, Hkv, d, device):
 
 
 def paged_decode_shared_workspace_size(R, Hq, Hkv, d, max_prefix_blocks, max_blocks_per_seq, block_size) -> int:
-    return _size("fa_paged_decode_shared_workspace_size", R, Hq, Hkv, d, max_prefix_blocks, max_blocks_per_seq, block_size)
+    return _size("fa_paged_decode_shared_workspace_size", R, Hq, Hkv, d, max_prefix_blocks, max_blocks_per_seq,
+                 block_size)
 
 
 def _decode_outputs(q, shape, device, with_lse, out):
@@ -624,8 +624,8 @@ def paged_evict(k_cache, v_cache, block_table, ctx_lens, seq_lens, weights, slot
     nc = _expect("new_ctx", new_ctx, (R,), i32, device)
     need = _size("fa_paged_evict_workspace_size", R, Hkv, maxb, keep)
     ws, ws_bytes, alive = _workspace(workspace, need, k_cache)
-    _call("fa_paged_evict", device, kc, vc, bt, ctx, seq, w, sp, wo, so, nc, ws, ws_bytes, R, Hkv, d, bs, maxb, num_blocks,
-          keep, recent, FA_DTYPE_BF16)
+    _call("fa_paged_evict", device, kc, vc, bt, ctx, seq, w, sp, wo, so, nc, ws, ws_bytes, R, Hkv, d, bs, maxb,
+          num_blocks, keep, recent, FA_DTYPE_BF16)
     return new_ctx, weights_out, slot_pos_out
 
 

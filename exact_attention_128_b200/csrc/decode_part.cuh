@@ -222,16 +222,18 @@ __global__ void __launch_bounds__(part::WARPS * 32)
         for (int e = 0; e < 4; ++e)
           if (nt * 8 + 2 * t4 + (e & 1) >= valid) sc[nt][e] = -INFINITY;
     }
+    const float old0 = m0, old1 = m1;
     float mx0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
     float mx1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);  // every block has a cached token
-    const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1);
-    m0 = n0;
-    m1 = n1;
+    m0 = fmaxf(m0, mx0);
+    m1 = fmaxf(m1, mx1);
+    // (scores of -inf alone so far, from keys with infinities: their mass is 0)
+    const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
+    const float a0 = ex2(old0 - n0), a1 = ex2(old1 - n1);
     float pr[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(part::WARPS * 32)
       U += so[(w * ROWS + i) * C::OP + d] * wt;
     }
     const size_t pi = size_t(row_of(i)) * p.parts + part;
-    p.part_o[pi * D + d] = U / L;
+    p.part_o[pi * D + d] = L == 0.f ? 0.f : U / L;  // (no mass: lse = -inf)
     if (d == 0) p.part_lse[pi] = M + __log2f(L);
   }
   finish();

@@ -36,6 +36,7 @@ class Prepared {
 };
 
 constexpr int kSms = 148;  // SMs that work is divided for
+constexpr int kMaxTokens = 1 << 30;  // of a table, so that token indexes plus a grid's stride stay below 2^31
 
 // Rotation arguments that every rotary entry point shares: sizes, then one of `out` launches.
 fa_status rope_check(const int* positions, const double* inv_freq, int B, int Hq, int Hkv, int N, int d, int rotary_dim,
@@ -305,7 +306,7 @@ fa_status part_check(const void* q, const void* k_cache, const void* v_cache, co
     return FA_ERR_INVALID_ARG;
   if (dtype != FA_DTYPE_BF16 || (d != 64 && d != 128) || block_size != part::BS) return FA_ERR_UNSUPPORTED;
   if (Hq / Hkv > part::ROWS || R > 65535 || Hkv > 65535 || int64_t(R) * Hq > 0x7fffffff) return FA_ERR_UNSUPPORTED;
-  if (int64_t(num_blocks) * Hkv * part::BS > 0x7fffffff || int64_t(max_blocks) * part::BS > 0x7fffffff)
+  if (int64_t(num_blocks) * Hkv * part::BS > 0x7fffffff || int64_t(max_blocks) * part::BS > kMaxTokens)
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -390,7 +391,7 @@ fa_status fa_qk_norm_rope_append(const fa_qk_norm_rope_append_args* args, void* 
   if (s != FA_OK) return s;
   if (a.block_size <= 0 || a.max_blocks_per_seq <= 0 || a.num_blocks <= 0) return FA_ERR_INVALID_ARG;
   if (a.dtype != FA_DTYPE_BF16 || a.d == 256 || a.block_size != 16) return FA_ERR_UNSUPPORTED;
-  if (int64_t(a.max_blocks_per_seq) * 16 > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  if (int64_t(a.max_blocks_per_seq) * 16 > kMaxTokens) return FA_ERR_UNSUPPORTED;
   if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) ||
       !rope_rows(a.v, a.v_strides, a.dtype))
     return FA_ERR_INVALID_ARG;
@@ -487,7 +488,7 @@ fa_status fa_paged_decode_shared(const fa_paged_decode_shared_args* args, void* 
   const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
                                  a.d, a.block_size, a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
   if (s != FA_OK) return s;
-  if (int64_t(a.max_prefix_blocks) * part::BS > 0x7fffffff) return FA_ERR_UNSUPPORTED;
+  if (int64_t(a.max_prefix_blocks) * part::BS > kMaxTokens) return FA_ERR_UNSUPPORTED;
   return part_call(a.q, a.k_cache, a.v_cache, a.prefix_table, a.prefix_len, a.block_table, a.ctx_lens, nullptr, a.o,
                    a.lse, a.R, a.Hq, a.Hkv, a.d, a.max_prefix_blocks, a.max_blocks_per_seq, a.num_blocks, a.scale,
                    a.workspace, a.workspace_bytes, stream);
@@ -536,7 +537,7 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
     return FA_ERR_INVALID_ARG;
   if (a.dtype != FA_DTYPE_BF16 || (a.d != 64 && a.d != 96 && a.d != 128 && a.d != 256) || a.block_size != evict::BS)
     return FA_ERR_UNSUPPORTED;
-  if (a.R > 65535 || a.Hkv > 65535 || int64_t(a.max_blocks_per_seq) * evict::BS > 0x7fffffff ||
+  if (a.R > 65535 || a.Hkv > 65535 || int64_t(a.max_blocks_per_seq) * evict::BS > kMaxTokens ||
       int64_t(a.num_blocks) * a.Hkv * evict::BS > 0x7fffffff)
     return FA_ERR_UNSUPPORTED;
   const EvictPlan n = evict_plan(a.R, a.Hkv, a.max_blocks_per_seq, a.keep);
@@ -546,8 +547,8 @@ fa_status fa_paged_evict(const fa_paged_evict_args* args, void* stream) {
   const EvictParams prm{a.block_table, a.ctx_lens, a.seq_lens, a.weights, a.slot_pos, a.weights_out, a.slot_pos_out,
                         a.new_ctx, reinterpret_cast<int*>(ws + n.off_moves), reinterpret_cast<int*>(ws),
                         reinterpret_cast<uint32_t*>(ws + n.off_masks), static_cast<uint4*>(a.k_cache),
-                        static_cast<uint4*>(a.v_cache), a.R, a.Hkv, a.max_blocks_per_seq, a.num_blocks, a.keep, a.recent,
-                        n.cap, a.d * 2 / 16, n.in_smem, n.fused};
+                        static_cast<uint4*>(a.v_cache), a.R, a.Hkv, a.max_blocks_per_seq, a.num_blocks, a.keep,
+                        a.recent, n.cap, a.d * 2 / 16, n.in_smem, n.fused};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t M = int64_t(a.max_blocks_per_seq) * evict::BS;
   const int smem = n.in_smem ? int((M + 2 * ((M + 31) / 32)) * 4) : 0;

@@ -16,8 +16,7 @@
 // from shared memory, as they share the weights.  (With the angles of a lane's 8 pairs computed by
 // each warp for itself and kept in registers, 116 registers left 16 warps on an SM, and the
 // 8192-token prefill of 4 x 40 heads took 115 us instead of 111, the fp32 image layer 33 instead of
-// 29.)  A warp writes 1 KB of
-// consecutive tokens of one head.
+// 29.)  A warp writes 1 KB of consecutive tokens of one head.
 //
 // Angles: the position (up to 2^31) times the frequency is taken in turns in 64 bits and reduced
 // to [-1/2, 1/2] before it is rounded to 32 bits, so far positions lose nothing; no table of
@@ -349,8 +348,8 @@ __global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
   for (int g = 0; g < p.groups; ++g) {
     const int tt = (int(blockIdx.x) * p.groups + g) * C::TOKENS + lane / C::L;
     const int bb = tt < tokens ? tt / p.N : 0, nn = tt < tokens ? tt - bb * p.N : 0;
-    table_entry<INTER>(s_table + g * TABLE, lane, warp, runs, p.pos + bb * p.pos_sb + nn, p.pos_sa, p.freq, p.rd, p.sec0,
-                       p.sec1, c < C::PAIRS && tt < tokens);
+    table_entry<INTER>(s_table + g * TABLE, lane, warp, runs, p.pos + bb * p.pos_sb + nn, p.pos_sa, p.freq, p.rd,
+                       p.sec0, p.sec1, c < C::PAIRS && tt < tokens);
   }
   if (norm) {
     fill_weights<T, D, SPREAD>(s_w, p.w[0], p.rd);
@@ -437,7 +436,8 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
   for (int e = 0; e < 8; ++e) sum[e] = both(0.f);
   if (norm) load_weights<T>(p.w[kind], runs, w);
 
-  for (int64_t unit = int64_t(cta) * (THREADS / 32) + warp_id(); unit < units; unit += int64_t(n_cta) * (THREADS / 32)) {
+  constexpr int WARPS = THREADS / 32;
+  for (int64_t unit = int64_t(cta) * WARPS + warp_id(); unit < units; unit += int64_t(n_cta) * WARPS) {
     const int tg = int(unit / chunks), h0 = int(unit - int64_t(tg) * chunks) * p.chunk[kind],
               h1 = min(H, h0 + p.chunk[kind]);
     const int t = tg * C::TOKENS + lane / C::L;

@@ -83,10 +83,10 @@ struct PrefixBars {
 };
 static_assert(sizeof(PrefixBars) <= 256, "barrier area");
 
-// (launched with fewer threads than its bound: 608 threads leave 104 registers to each, so that the
-// register file holds a CTA of the requests' own part too)
+// (104 registers, so that the register file holds a CTA of the requests' own part too: 96 and 112
+// take the same time, with 120 it does not fit beside this one: 139 -> 142 us for 256 requests)
 template <int D>
-__global__ void __launch_bounds__(608)
+__global__ void __maxnreg__(104)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefixParams p) {
   using C = PrefixCfg<D>;
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(608)
           for (int c = 16; c < C::BN; c += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], f[c + k], f[c + 8 + k]);
-          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmaxf(fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
           // the reference of l and u moves only when the maximum passes it by FA_RESCALE_LOG2 (see the forward kernel)
           const float m_cand = fmaxf(m, mx * sl2);
           const float m_new = (m_cand > m + FA_RESCALE_LOG2) ? m_cand : m;
@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(608)
           const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
           l = l * alpha + (rsa.x + rsa.y);
           if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // u must hold the tile before this one, and no later one can have been added yet 
-            if (!(ok = warp_wait(&bars->v_empty[(g - 1) % C::NSTAGE], ((g - 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag,
-                                 332 + t))) break;
+            // u must hold the tile before this one, and no later one can have been added yet
+            ok = warp_wait(&bars->v_empty[(g - 1) % C::NSTAGE], ((g - 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag, 332 + t);
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -371,13 +371,14 @@ __global__ void __launch_bounds__(608)
         if (lane == 0) mbar_arrive(&bars->p_full[t][g & 1]);
       }
       // P V of the item's last step
-      if (ok) ok = warp_wait(&bars->v_empty[(g - 1) % C::NSTAGE], ((g - 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag, 340 + t);
+      if (ok)
+        ok = warp_wait(&bars->v_empty[(g - 1) % C::NSTAGE], ((g - 1) / C::NSTAGE) & 1, p.wait_ns, abort_flag, 340 + t);
       if (!ok) break;
       if (idle) continue;
       tc_fence_after();
       // u / l: 16 columns at a time through the warp's staging (16-byte pieces swizzled by the row),
       // so that four lanes write 64 consecutive bytes of a row
-      const float inv = 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (scores of -inf alone: lse = -inf, no share in the row)
       const int part = int(blockIdx.x) - deal.owner((long long)(it)*deal.nt);
       const size_t row0 = ((size_t(it) * p.parts + part) * 2 + t) * C::BM + wq * 32;
       uint8_t* stg = smem + C::OFF_STG + (warp - 2) * C::STG_WARP;

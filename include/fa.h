@@ -361,7 +361,8 @@ size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int 
  *   Either length may be 0, up to its table's capacity; a request with no token at all gets
  *   o = 0 and lse = -inf.  Table entries past a length's last block are never read.
  *   o [R,Hq,d] bf16, lse [R,Hq] fp32 or NULL (natural log).
- *   d in {64, 128}, block_size == 16, Hq / Hkv <= 16, dtype BF16.
+ *   d in {64, 128}, block_size == 16, Hq / Hkv <= 16, dtype BF16; tables of up to 2^30 tokens (so
+ *   in every call below, and in fa_qk_norm_rope_append).
  *   A length out of range or a bad block id is not dereferenced and sets the device status word
  *   (FA_ERR_INVALID_ARG); the results it belongs to are undefined.
  * Errors: FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE.

@@ -156,3 +156,12 @@ def test_binding_rejects_cpu_tensors():
     for bad in (0, 7, -2):
         with pytest.raises(ValueError):
             fa.rope_frequencies(bad, device="cpu")
+
+
+@pytest.mark.parametrize("name,base,kw", [
+    ("fa_qk_norm_rope_append", APPEND, dict(maxb=(1 << 26) + 1)), ("fa_paged_decode_shared", SHARED, dict(pb=(1 << 26) + 1)),
+    ("fa_paged_decode_shared", SHARED, dict(maxb=(1 << 26) + 1)), ("fa_paged_decode_scored", SCORED, dict(maxb=(1 << 26) + 1)),
+    ("fa_paged_evict", EVICT, dict(maxb=(1 << 26) + 1))])
+def test_tables_of_more_than_2_30_tokens_are_refused(L, name, base, kw):
+    """A kernel's token index plus its grid's stride stays inside 32 bits."""
+    assert call(L, name, base, kw) == UNS

@@ -11,6 +11,8 @@ turned value g = a cos t - b sin t may cancel: cos and sin are off by 2^-22.3 (t
 rounded to 2^-25 turns, times 2 pi) + 2^-23 (the function), the two products and the difference by 2^-24 each, so g is
 off by at most 2^-21 (|a| + |b|) however small it is, and the sum by 2^-21 sum (|a| + |b|) |n| more.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -349,6 +351,57 @@ def test_decode_scored(d, Hq, Hkv, lens):
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(w, w2)
 
 
+def minus_infinity(q, kc, rows):
+    """Scores of -inf for the tokens of these (block, slots), by keys of -inf where q is positive."""
+    q[..., 0] = q[..., 0].abs() + 1
+    for block, slots in rows:
+        kc[block, :, slots, 0] = -math.inf
+    return kc.nan_to_num(0.0, 0.0, 0.0)  # for the bounds: every other key
+
+
+@pytest.mark.parametrize("wide", [0, 800])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dead,prefix", [(128, 300), (64, 64), (1, 40), (299, 300)])
+def test_shared_scores_of_minus_infinity(d, dead, prefix, wide):
+    """Keys without weight: a tile's, a piece's and a whole prefix's, and every own one of a request."""
+    lens = (40, 16, 3) + (5,) * 22
+    q, kc, vc, table, ptable, ctx = decode_case(lens, 12, 4, d, 40, 640 + d + prefix, prefix)
+    rows = [(ptable[b], slice(0, min(16, dead - 16 * b))) for b in range(-(-dead // 16))]
+    rows += [(table[0, 0], slice(0, 16))]
+    if dead < prefix:
+        rows += [(table[1, 0], slice(0, 16))]
+    finite = minus_infinity(q, kc, rows)
+    ptable = torch.cat([ptable, torch.full((wide,), -1, dtype=torch.int32)])
+    o, lse = fa.paged_decode_shared(*(t.cuda() for t in (q, kc, vc, ptable, torch.tensor([prefix], dtype=torch.int32),
+                                                         table, ctx)))
+    clean()
+    O, L = ops.decode_shared(q, kc, vc, ptable, prefix, table, ctx, 16, d**-0.5)
+    assert np.isfinite(O).all() and np.isfinite(L).all()
+    delta, slack = bounds(q, finite, vc, d**-0.5)
+    V, _ = ops.decode_shared(q, kc, vc.abs(), ptable, prefix, table, ctx, 16, d**-0.5)
+    near(o, O, slack + 2.0**-8 * V, "o")
+    near(lse, L, delta + 2.0**-20 * np.abs(L), "lse")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_scored_scores_of_minus_infinity(d):
+    lens = (300, 17, 640)
+    q, kc, vc, table, _, ctx = decode_case(lens, 8, 2, d, 40, 740 + d)
+    rows = [(table[0, b], slice(0, 16)) for b in range(8)] + [(table[1, 0], slice(0, 16))]
+    rows += [(table[2, b], slice(3, 12)) for b in range(40)]
+    finite = minus_infinity(q, kc, rows)
+    w0 = randn((3, 2, 640), 10, F32).abs()
+    w = w0.cuda()
+    o, lse = fa.paged_decode_scored(*(t.cuda() for t in (q, kc, vc, table, ctx)), w)
+    clean()
+    O, L, W = ops.decode_scored(q, kc, vc, table, ctx, w0, 16, d**-0.5)
+    assert np.isfinite(O).all() and np.isfinite(L).all()
+    delta, slack = bounds(q, finite, vc, d**-0.5)
+    near(o, O, slack, "o")
+    near(lse, L, delta + 2.0**-20 * np.abs(L), "lse")
+    near(w, W, (2 * delta + 2.0**-19) * (W - ora.to_f64(w0)), "weights")
+
+
 def test_decode_flags_bad_lengths_and_blocks():
     q, kc, vc, table, ptable, ctx = decode_case((20, 20, 20), 4, 2, 128, 4, 31, 40)
     table[1, 0] = kc.shape[0]
@@ -469,3 +522,28 @@ def test_refusals_of_the_binding():
     with pytest.raises(fa.FAError):  # in place
         fa.paged_evict(kc, vc, table, ctx, ctx, w, sp, 4, 2, weights_out=w)
     torch.cuda.synchronize()
+
+
+def test_refusals_of_numbers():
+    """Sizes that are no integers, or that do not fit the C type they are passed in."""
+    _, kc, vc, table, _, ctx = (t.cuda() for t in decode_case((20, 3), 4, 2, 128, 4, 53))
+    w, sp = torch.zeros(2, 2, 64, device="cuda"), torch.full((2, 2, 64), -1, device="cuda", dtype=torch.int32)
+    for keep, recent in ((4.5, 2), (2**32 + 4, 2), (4, 2**40)):
+        with pytest.raises(ValueError):
+            fa.paged_evict(kc, vc, table, ctx, ctx, w, sp, keep, recent)
+    torch.cuda.synchronize()
+
+
+def test_gradients_of_broadcast_inputs():
+    """q, k shared by heads and batches through strides of 0: one gradient row for each, dense."""
+    _, _, _, (wq, wk), pos, freq = rope_inputs(2, 4, 2, 5, 64, 64, (32,), BF, True, 54)
+    q, k = randn((2, 1, 5, 64), 55, BF).cuda(), randn((1, 1, 1, 64), 56, BF).cuda()
+    dq, dk = randn((2, 4, 5, 64), 57, BF).cuda(), randn((2, 2, 5, 64), 58, BF).cuda()
+    args = (wq, wk, pos, freq)
+    wide = [t.expand(2, h, 5, 64) for t, h in ((q, 4), (k, 2))]
+    got = fa.qk_norm_rope_bwd(dq, dk, *wide, *args)
+    ref = fa.qk_norm_rope_bwd(dq, dk, *(t.contiguous() for t in wide), *args)
+    clean()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    for a, b in zip(fa.qk_norm_rope(*wide, *args), fa.qk_norm_rope(*(t.contiguous() for t in wide), *args)):
+        assert torch.equal(a, b)
