@@ -13,7 +13,9 @@
 // What bounds it: reading K and V once.  Four warps take every fourth block, each with its own
 // ring of TMA stages and its own (m, l, u); rows sit in the 16 rows of mma.sync m16n8k16.
 // P is multiplied as the sum of two bf16 parts, its rounding and the rest: the tensor cores idle
-// here, and with it the output's only rounding is the last one.
+// here, and with it the output's only rounding is the last one.  64 requests of 512 to 8192 tokens, 2
+// kv heads, d = 128 (286 MB): 56 us, 5.1 TB/s; with scores (13 MB more) 58 us.  The join takes 9 us
+// behind it: it is a chain of four dependent loads (lengths, lse of the pieces, results, old weights).
 #pragma once
 #include "decode.cuh"
 

@@ -23,7 +23,8 @@
  *     16-byte aligned.  The caller owns every buffer, workspaces included; the library
  *     never allocates device memory.  Its only state between calls is the process-wide
  *     settings of fa_set_wait_limit_ns and fa_set_decode_split and, for
- *     fa_paged_decode_noalloc, the cached address of its scratch array.
+ *     fa_paged_decode_noalloc, the cached address of its scratch array; and, for kernels that
+ *     need launch attributes, on which devices these have been set.
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*; NULL is the
  *     legacy default stream).  FA_OK means the launch was accepted.  Faults that
  *     happen while the kernel runs surface at the caller's next synchronisation.

@@ -117,3 +117,46 @@ def test_eviction_keeps_the_recent_and_the_heavy():
     # a second call with nothing appended changes nothing
     again = ops.evict(k2, v2, table, n2, seq, w2, p2, keep, recent, 4)
     assert all(np.array_equal(a, b) for a, b in zip(again, (k2, v2, n2, w2, p2)))
+
+
+def test_turn_by_hand():
+    """A quarter turn takes (1, 0) to (0, 1) and (0, 1) to (-1, 0); where the pair lies is all that differs."""
+    for inter, pair in ((False, (1, 5)), (True, (2, 3))):  # pair 1 of a rotary width of 8
+        x = np.zeros((1, 1, 2, 10))
+        x[0, 0, 0, pair[0]], x[0, 0, 1, pair[1]], x[..., 9] = 1, 1, 7
+        freq = np.array([0.1, np.pi / 6, 0.2, 0.3])
+        y = ops.norm_rope(x, None, np.full((1, 1, 2), 3), freq, (4,), inter, 1e-6)
+        want = np.zeros_like(x)
+        want[0, 0, 0, pair[1]], want[0, 0, 1, pair[0]], want[..., 9] = 1, -1, 7
+        assert np.allclose(y, want, atol=1e-15)
+
+
+def test_append_is_the_norm_then_one_cache_write_a_token():
+    kc, vc, table, _, g = cache(d=16)
+    q, k, v = g.standard_normal((3, 4, 3, 16)), *g.standard_normal((2, 3, 2, 3, 16))
+    w, pos, freq = 1 + 0.1 * g.standard_normal((2, 16)), g.integers(0, 99, (1, 3, 3)), 0.3 ** np.arange(8)
+    ctx, ql, out = np.array([20, 6, 4]), np.array([3, 2, 0]), np.full(q.shape, 9.0)
+    Q, K, V = ops.norm_rope_append(q, k, v, *w, pos, freq, (8,), False, 1e-6, kc, vc, table, ctx, ql, out, 4)
+    qn, kn = (ops.norm_rope(x, u, pos, freq, (8,), False, 1e-6) for x, u in zip((q, k), w))
+    k2, v2 = kc, vc
+    for r in range(3):
+        for i in range(ql[r]):
+            k2, v2 = ora.paged_append(k2, v2, table[r : r + 1], ctx[r : r + 1] - ql[r] + i, kn[r : r + 1, :, i],
+                                      v[r : r + 1, :, i], 4)
+        assert np.array_equal(Q[r, :, : ql[r]], qn[r, :, : ql[r]]) and (Q[r, :, ql[r] :] == 9).all()
+    assert np.array_equal(K, k2) and np.array_equal(V, v2)
+
+
+def test_attention_after_an_eviction_is_that_of_the_kept_tokens():
+    kc, vc, table, _, g = cache()
+    ctx, w, sp = np.array([18, 9, 5]), g.random((3, 2, 20)), np.full((3, 2, 20), -1)
+    k2, v2, n2, _, p2 = ops.evict(kc, vc, table, ctx, ctx, w, sp, 8, 3, 4)
+    q = g.standard_normal((3, 2, 8))
+    o, lse = ora.paged_decode(q, k2, v2, table, n2, 4, 0.3)
+    for r in range(3):
+        for h in range(2):
+            kept = sorted(p2[r, h, : n2[r]])  # in their old order; a first eviction: positions are slots
+            k, v = (ora.depage(c, table[r], ctx[r], h, 4)[kept] for c in (kc, vc))
+            s = 0.3 * k @ q[r, h]
+            p = np.exp(s - s.max())
+            assert np.allclose(o[r, h], p @ v / p.sum()) and np.isclose(lse[r, h], np.log(p.sum()) + s.max())
