@@ -1,4 +1,6 @@
 """The entry points of the passes around attention refuse bad arguments on the host.  Runs without a GPU."""
+import struct
+
 import pytest
 import torch
 
@@ -7,6 +9,16 @@ from exact_attention_128_b200 import build as fabuild
 
 FAKE = 1 << 20  # 16-byte aligned, never dereferenced: every call below is rejected on the host
 BAD, UNS, WS = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_ERR_WORKSPACE
+
+# the argument structs of fa.h: pointers and sizes, int64 strides, ints, eps or scale, ints
+PACKED = {
+    "fa_qk_norm_rope": struct.Struct("8P8q11ifi"),
+    "fa_qk_norm_rope_append": struct.Struct("13P11q14ifi"),
+    "fa_qk_norm_rope_bwd": struct.Struct("14P14q11if3i"),
+    "fa_paged_decode_shared": struct.Struct("11P8ifi"),
+    "fa_paged_decode_scored": struct.Struct("10P7ifi"),
+    "fa_paged_evict": struct.Struct("12P9i"),
+}
 
 
 @pytest.fixture(scope="module")
@@ -21,7 +33,7 @@ def call(L, name, base, kw):
     flat = []
     for v in {**base, **kw}.values():
         flat += v if isinstance(v, (list, tuple)) else [0 if v is None else v]
-    return getattr(L, name)(fa.PACKED[name](*flat), None)
+    return getattr(L, name)(PACKED[name].pack(*flat), None)
 
 
 SX, ROW = (32, 0, 0), (2048, 64, 512)  # sections; strides of [1, 4, 4, 64] in a projection
@@ -108,16 +120,16 @@ def test_evict_rejects_on_host(L, kw, code):
 
 
 def test_null_struct_is_refused(L):
-    for name in fa.PACKED:
+    for name in PACKED:
         assert getattr(L, name)(None, None) == BAD
 
 
 def test_structs_match_the_header(L, tmp_path):
-    """The binding's packers fill exactly the C structs: their sizes, and one field near each end."""
+    """PACKED fills exactly the C structs: their sizes, and one field near each end."""
     import os
     import subprocess
 
-    names = list(fa.PACKED)
+    names = list(PACKED)
     body = "".join(f'printf("%zu %zu\\n", sizeof({n}_args), offsetof({n}_args, dtype));' for n in names)
     src = tmp_path / "s.c"
     src.write_text('#include <stdio.h>\n#include "fa.h"\nint main(void){' + body + "return 0;}")
@@ -126,7 +138,7 @@ def test_structs_match_the_header(L, tmp_path):
     out = subprocess.run([str(tmp_path / "s")], check=True, capture_output=True, text=True).stdout.split()
     for i, n in enumerate(names):
         size, at = int(out[2 * i]), int(out[2 * i + 1])
-        packed = fa.PACKED[n].__self__
+        packed = PACKED[n]
         last = 2 if n == "fa_qk_norm_rope_bwd" else 0  # ints behind dtype
         assert packed.size + (-packed.size) % 8 == size and at == packed.size - 4 * (1 + last), n
 
