@@ -14,6 +14,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <array>
 #include <climits>
@@ -53,8 +54,8 @@ std::string described(PyObject* o) {
 }
 
 const Tensor& tensor(PyObject* o, const char* name, int64_t dim) {
-  TORCH_CHECK_VALUE(THPVariable_Check(o) && THPVariable_Unpack(o).dim() == dim, name, " must be a CUDA tensor of ", dim,
-                    " dimensions, got ", described(o));
+  TORCH_CHECK_VALUE(THPVariable_Check(o) && THPVariable_Unpack(o).dim() == dim, name, " must be a CUDA tensor of ",
+                    dim, " dimensions, got ", described(o));
   return THPVariable_Unpack(o);
 }
 
@@ -159,11 +160,12 @@ struct Workspace {
       bytes = need;
       return;
     }
-    TORCH_CHECK_VALUE(THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda() &&
-                          THPVariable_Unpack(o).get_device() == like.get_device() && THPVariable_Unpack(o).is_contiguous(),
+    TORCH_CHECK_VALUE(THPVariable_Check(o), "workspace must be a tensor, got ", described(o));
+    const Tensor& t = THPVariable_Unpack(o);
+    TORCH_CHECK_VALUE(t.is_cuda() && t.get_device() == like.get_device() && t.is_contiguous(),
                       "workspace must be a contiguous tensor on ", like.device(), ", got ", described(o));
-    at = THPVariable_Unpack(o).data_ptr();
-    bytes = THPVariable_Unpack(o).nbytes();
+    at = t.data_ptr();
+    bytes = t.nbytes();
   }
 };
 
@@ -172,9 +174,10 @@ template <typename A>
 void call(const char* name, fa_status (*fn)(const A*, void*), const A& args, int64_t device) {
   fa_status status;
   {
-    const c10::cuda::OptionalCUDAGuard guard(
-        c10::cuda::current_device() == device ? c10::nullopt : c10::optional<c10::Device>(c10::Device(at::kCUDA, device)));
-    void* stream = c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(device)).stream();
+    const c10::DeviceIndex index(static_cast<c10::DeviceIndex>(device));
+    c10::cuda::OptionalCUDAGuard guard;
+    if (c10::cuda::current_device() != index) guard.set_index(index);
+    void* stream = c10::cuda::getCurrentCUDAStream(index).stream();
     Py_BEGIN_ALLOW_THREADS;
     status = fn(&args, stream);
     Py_END_ALLOW_THREADS;
@@ -208,12 +211,13 @@ void rope_arguments(A& a, PyObject* positions, PyObject* inv_freq, PyObject* sec
   const int64_t half = tensor(inv_freq, "inv_freq", 1).size(0);
   a.inv_freq = expect<const double>(inv_freq, "inv_freq", {half}, at::kDouble, device);
   a.rotary_dim = size32(2 * half, "rotary_dim");
-  TORCH_CHECK_VALUE(THPVariable_Check(positions), "positions must be [N], [B,N] or [axes,B,N], got ", described(positions));
+  TORCH_CHECK_VALUE(THPVariable_Check(positions), "positions must be a tensor, got ", described(positions));
   const Tensor& t = THPVariable_Unpack(positions);
   const int64_t dims = t.dim(), axes = dims == 3 ? t.size(0) : 1;
   const std::array<int64_t, 3> want{axes, B, N};
-  TORCH_CHECK_VALUE(dims >= 1 && dims <= 3 && t.sizes() == IntArrayRef(want).slice(3 - dims), "positions must be [N], [B,N] ",
-                    "or [axes,B,N] with B = ", B, " and N = ", N, ", got ", described(positions));
+  TORCH_CHECK_VALUE(dims >= 1 && dims <= 3 && t.sizes() == IntArrayRef(want).slice(3 - dims),
+                    "positions must be [N], [B,N] or [axes,B,N] with B = ", B, " and N = ", N, ", got ",
+                    described(positions));
   TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.is_cuda() && t.get_device() == device &&
                         (N <= 1 || t.stride(dims - 1) == 1),
                     "positions must be int32 on device ", device, " with a contiguous last dimension, got ",
@@ -228,21 +232,11 @@ void rope_arguments(A& a, PyObject* positions, PyObject* inv_freq, PyObject* sec
     a.sections[0] = int(half);
     sum = axes == 1 ? half : -1;
   } else {
-    PyObject* list = PySequence_Fast(sections, "sections must be a sequence");
+    const THPObjectPtr list(PySequence_Fast(sections, "sections must be a sequence of integers"));
     if (!list) throw python_error();
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
-    std::array<int, 3> got{};
-    for (Py_ssize_t i = 0; i < n && i < 3; ++i) {
-      PyObject* item = PySequence_Fast_GET_ITEM(list, i);
-      got[i] = PyLong_Check(item) ? int(std::min<long long>(std::max<long long>(PyLong_AsLongLong(item), INT_MIN), INT_MAX))
-                                  : INT_MIN;
-      PyErr_Clear();
-    }
-    Py_DECREF(list);
-    for (int i = 0; i < 3; ++i) {
-      a.sections[i] = got[i];
-      sum += got[i];
-    }
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list.get());
+    for (Py_ssize_t i = 0; i < n && i < 3; ++i)
+      sum += a.sections[i] = integer(PySequence_Fast_GET_ITEM(list.get(), i), "a section");
     if (n != axes) sum = -1;
   }
   TORCH_CHECK_VALUE(sum == half, axes, " axes of positions need as many sections that sum to ", half);
@@ -283,7 +277,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* o, Py_ssize_t) {
   END_HANDLE_TH_ERRORS
 }
 
-// dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps, grad_dtype, dq, dk, workspace
+// dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, sections, interleaved, eps, grad_dtype, dq, dk,
+// workspace
 PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* o, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Tensor& q = first_tensor(o[2], "q", 4);
@@ -296,7 +291,8 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* o, Py_ssize_t) {
   const ScalarType grad = o[11] == Py_None ? dtype : reinterpret_cast<THPDtype*>(o[11])->scalar_type;
   const std::array<int64_t, 4> shape{B, Hq, N, d}, kshape{B, Hkv, N, d};
   fa_qk_norm_rope_bwd_args a = {};
-  a.dtype = dtype_code(dtype, "q"), a.dout_dtype = dtype_code(dout, "dq_out"), a.grad_dtype = dtype_code(grad, "grad_dtype");
+  a.dtype = dtype_code(dtype, "q");
+  a.dout_dtype = dtype_code(dout, "dq_out"), a.grad_dtype = dtype_code(grad, "grad_dtype");
   a.q = rows(o[2], "q", shape, dtype, device, a.q_strides);
   a.k = rows(o[3], "k", kshape, dtype, device, a.k_strides);
   a.dq_out = expect(o[0], "dq_out", shape, dout, device);
@@ -430,16 +426,16 @@ PyObject* paged_decode_scored(PyObject*, PyObject* const* o, Py_ssize_t) {
   cache_arguments(a, o[1], o[2], o[3], o[4], s.R, s.Hkv, s.d, s.device);
   const int64_t M = int64_t(a.max_blocks_per_seq) * a.block_size;
   a.weights = expect<float>(o[5], "weights", {s.R, s.Hkv, M}, at::kFloat, s.device);
-  const Workspace ws(o[8], api.paged_decode_scored_workspace_size(a.R, a.Hq, a.Hkv, a.d, a.max_blocks_per_seq, a.block_size),
-                     s.q);
+  const Workspace ws(o[8], api.paged_decode_scored_workspace_size(a.R, a.Hq, a.Hkv, a.d, a.max_blocks_per_seq,
+                                                                  a.block_size), s.q);
   a.workspace = ws.at, a.workspace_bytes = ws.bytes;
   call("fa_paged_decode_scored", api.paged_decode_scored, a, s.device);
   return s.results();
   END_HANDLE_TH_ERRORS
 }
 
-// k_cache, v_cache, block_table, ctx_lens, seq_lens, weights, slot_pos, keep, recent, weights_out, slot_pos_out, new_ctx,
-// workspace
+// k_cache, v_cache, block_table, ctx_lens, seq_lens, weights, slot_pos, keep, recent, weights_out, slot_pos_out,
+// new_ctx, workspace
 PyObject* paged_evict(PyObject*, PyObject* const* o, Py_ssize_t) {
   HANDLE_TH_ERRORS
   const Tensor& k = first_tensor(o[0], "k_cache", 4);
@@ -451,7 +447,8 @@ PyObject* paged_evict(PyObject*, PyObject* const* o, Py_ssize_t) {
   a.weights = expect<const float>(o[5], "weights", shape, at::kFloat, device);
   a.slot_pos = expect<const int>(o[6], "slot_pos", shape, at::kInt, device);
   a.keep = integer(o[7], "keep"), a.recent = integer(o[8], "recent");
-  Output weights_out(o[9], shape, k.options().dtype(at::kFloat)), slot_pos_out(o[10], shape, k.options().dtype(at::kInt));
+  Output weights_out(o[9], shape, k.options().dtype(at::kFloat));
+  Output slot_pos_out(o[10], shape, k.options().dtype(at::kInt));
   Output new_ctx(o[11], {R}, k.options().dtype(at::kInt));
   a.weights_out = weights_out.expect<float>("weights_out", shape, at::kFloat, device);
   a.slot_pos_out = slot_pos_out.expect<int>("slot_pos_out", shape, at::kInt, device);

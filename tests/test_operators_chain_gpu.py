@@ -312,3 +312,40 @@ def test_workspace_given_and_reused():
     with pytest.raises(fa.FAError):
         fa.paged_decode_shared(*case, workspace=torch.empty(need - 1, device="cuda", dtype=torch.uint8))
     assert fa.device_status() == 0
+
+
+def test_threads_call_at_once():
+    """Calls from several threads, each on its own stream, sizes of shared memory growing and shrinking between them."""
+    import threading
+
+    cases = [shared_case(R, P) for R, P in ((6, 200), (70, 800), (3, 40))]
+    ref = [fa.paged_decode_shared(*c) for c in cases]
+    sp = [torch.full((c[0].shape[0], 2, c[5].shape[1] * 16), -1, dtype=torch.int32, device="cuda") for c in cases]
+    caches = [(c[1].clone(), c[2].clone()) for c in cases]
+    w = [torch.rand(s.shape, generator=torch.Generator().manual_seed(i)).cuda() for i, s in enumerate(sp)]
+    kept = [fa.paged_evict(*(x.clone() for x in caches[i]), c[5], c[6], c[6], w[i], sp[i], 16 + i, 4)
+            for i, c in enumerate(cases)]
+    torch.cuda.synchronize()
+    got, failed = [[] for _ in cases], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(40):
+                    o = fa.paged_decode_shared(*cases[i])
+                    e = fa.paged_evict(*(x.clone() for x in caches[i]), *(cases[i][j] for j in (5, 6, 6)), w[i], sp[i],
+                                       16 + i, 4)
+                got[i] = [*o, *e]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # (a thread's exception does not reach the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for i in range(len(cases)):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], (*ref[i], *kept[i])))
+    assert fa.device_status() == 0
