@@ -20,7 +20,7 @@
 // device, a second kernel does.
 //
 // What bounds it: after long prompts, the rows that move (32 requests x 8 heads of 4097 to 8192 tokens,
-// keep 2048: 23 us of selection, then 66 us for about 390 MB of rows read and written, 5.9 TB/s); in
+// keep 2048: 22 us of selection, then 66 us for about 390 MB of rows read and written, 5.9 TB/s); in
 // steady eviction of up to 128 tokens of 2176 (64 x 2 heads: 10 us), the selection's latency: two
 // passes over the weights, five over shared memory, a dozen barriers.
 #pragma once
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   extern __shared__ uint32_t evict_smem[];
   __shared__ __align__(16) int s_hist[BINS];
   __shared__ int4 s_warp[THREADS / 128];
-  __shared__ int s_found[2];  // the digit's bin, and how many of its tokens are still needed
+  __shared__ int s_found[3];  // the digit's bin, how many of its tokens are needed, and how many it has
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (the second kernel's CTAs, held ready on the SMs, left it 10 us slower)
   if (p.fused) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
   }
   auto key_of = [&](int s) { return p.in_smem ? s_key[s] : key_from(s, __ldg(w + s), __ldg(sp + s)); };
 
-  // the keep-th largest key, digit by digit; `need` of the tokens that have it are kept
+  // A threshold: keys above it are kept, and `need` of the tokens at it.  The keep-th largest key, digit
+  // by digit, or the key below the last bin where that bin is kept whole.
   uint32_t thr = 0;
   int need = p.keep;
 #pragma unroll
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
         if (before < need && need <= before + c[i]) {
           s_found[0] = top - i;
           s_found[1] = need - before;
+          s_found[2] = c[i];
         }
         before += c[i];
       }
@@ -232,6 +234,11 @@ __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const _
     __syncthreads();
     thr |= uint32_t(s_found[0]) << shift;
     need = s_found[1];
+    if (need == s_found[2]) {  // all of the bin: the digits below it do not matter
+      thr -= 1;                // (> 0: not every token is kept)
+      need = 0;
+      break;
+    }
   }
 
 #pragma unroll 4
