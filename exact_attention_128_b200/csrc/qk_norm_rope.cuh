@@ -38,12 +38,13 @@ constexpr int MAX_CHUNK = 16;  // backward: heads of a unit, at most
 constexpr int FWD_STAGES = 5, FWD_STAGES_F32 = 4, FWD_CTAS = 3;
 constexpr int BWD_STAGES = 4, BWD_CTAS = 2;
 
-// Lanes of one row: d / 16 rounded up to a power of two (d = 96: 6 of 8 lanes work).
+// Lanes of one row: d / 16.  (d = 96: 5 rows of 6 lanes, 2 lanes idle.  4 rows of 8 lanes with 6 at
+// work took 113 us forward and 160 backward for 4 x 8192 tokens of 32 + 8 heads, this way 101 and 149.)
 template <int D>
 struct Cfg {
-  static constexpr int PAIRS = D / 16;  // lanes that hold values
-  static constexpr int L = D == 96 ? 8 : D / 16;
-  static constexpr int TOKENS = 32 / L;  // tokens of a warp
+  static constexpr int L = D / 16;
+  static constexpr int TOKENS = 32 / L;       // tokens of a warp
+  static constexpr int WORK = L * TOKENS;     // its lanes that hold values
 };
 }  // namespace rope
 
@@ -241,7 +242,7 @@ __device__ __forceinline__ void table_entry(float4* table, int lane, int e, cons
 template <typename T, int D, bool SPREAD>
 __device__ __forceinline__ void fill_weights(float4* table, const void* w, int rd) {
   using C = Cfg<D>;
-  for (int i = threadIdx.x; i < C::PAIRS * 16; i += THREADS) {  // value v of lane l
+  for (int i = threadIdx.x; i < C::L * 16; i += THREADS) {  // value v of lane l
     const int l = i / 16, v = i % 16;
     const Runs<D, SPREAD> r(l, rd);
     reinterpret_cast<float*>(table + (v >> 2) * C::L + l)[v & 3] =
@@ -280,11 +281,33 @@ __device__ __forceinline__ void turn(float2 (&f)[8], const float2 (&c)[4], const
   }
 }
 
+// Sum over the lanes of a row, the same bits in each of them.
 template <int L>
 __device__ __forceinline__ float row_sum(float v) {
+  if constexpr (L == 6) {
+    const int lane = lane_id(), c = lane % 6, first = lane - c;
+    v += __shfl_sync(0xffffffffu, v, first + (c < 3 ? c + 3 : c - 3));
+    return __shfl_sync(0xffffffffu, v, first) + __shfl_sync(0xffffffffu, v, first + 1) +
+           __shfl_sync(0xffffffffu, v, first + 2);
+  } else {
 #pragma unroll
-  for (int m = 1; m < L; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
+    for (int m = 1; m < L; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+  }
+}
+// Sum over the rows of a warp, for each lane of the first row.
+template <int L>
+__device__ __forceinline__ float rows_sum(float v) {
+  if constexpr (L == 6) {
+    float sum = v;
+#pragma unroll
+    for (int k = 1; k < 5; ++k) sum += __shfl_down_sync(0xffffffffu, v, 6 * k);
+    return sum;
+  } else {
+#pragma unroll
+    for (int m = L; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+  }
 }
 
 }  // namespace rope
@@ -307,9 +330,9 @@ __global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
   const int sharers = 8 / p.groups, sub = warp / sharers;  // warps of a token group; this warp's group
   const int t = (int(blockIdx.x) * p.groups + sub) * C::TOKENS + lane / C::L;
   const int heads = p.Hq + p.Hkv + (PAGED ? p.Hkv : 0);
-  bool on = c < C::PAIRS && t < tokens;
+  bool on = lane < C::WORK && t < tokens;
   const int b = on ? t / p.N : 0, n = on ? t - b * p.N : 0;
-  const Runs<D, SPREAD> runs(c < C::PAIRS ? c : 0, p.rd);
+  const Runs<D, SPREAD> runs(c, p.rd);
   const bool norm = p.w[0] != nullptr;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
     const int tt = (int(blockIdx.x) * p.groups + g) * C::TOKENS + lane / C::L;
     const int bb = tt < tokens ? tt / p.N : 0, nn = tt < tokens ? tt - bb * p.N : 0;
     table_entry<INTER>(s_table + g * TABLE, lane, warp, runs, p.pos + bb * p.pos_sb + nn, p.pos_sa, p.freq, p.rd,
-                       p.sec0, p.sec1, c < C::PAIRS && tt < tokens);
+                       p.sec0, p.sec1, lane < C::WORK && tt < tokens);
   }
   if (norm) {
     fill_weights<T, D, SPREAD>(s_w, p.w[0], p.rd);
@@ -387,7 +410,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
         for (int e = 1; e < 8; ++e) sq = fma2(f[e], f[e], sq);
         const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
         float2 w[8];
-        read_planes(s_w + kind * 4 * C::L + (c < C::PAIRS ? c : 0), C::L, w);
+        read_planes(s_w + kind * 4 * C::L + c, C::L, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = mul2(f[e], mul2(r, w[e]));
       }
@@ -430,7 +453,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
   const int H = p.H[kind], chunks = p.chunks[kind];
   const int64_t units = int64_t((tokens + C::TOKENS - 1) / C::TOKENS) * chunks;
   const int lane = lane_id(), c = lane % C::L;
-  const Runs<D, SPREAD> runs(c < C::PAIRS ? c : 0, p.rd);
+  const Runs<D, SPREAD> runs(c, p.rd);
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -444,7 +467,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
     const int tg = int(unit / chunks), h0 = int(unit - int64_t(tg) * chunks) * p.chunk[kind],
               h1 = min(H, h0 + p.chunk[kind]);
     const int t = tg * C::TOKENS + lane / C::L;
-    const bool on = c < C::PAIRS && t < tokens;
+    const bool on = lane < C::WORK && t < tokens;
     const int b = on ? t / p.N : 0, n = on ? t - b * p.N : 0;
     const TG* dy = static_cast<const TG*>(p.dy[kind]) + (int64_t(b) * H * p.N + n) * D;
     const T* x = static_cast<const T*>(p.x[kind]) + b * p.sb[kind] + n * p.sn[kind];
@@ -507,13 +530,8 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float2 v = sum[e];
-#pragma unroll
-    for (int m = C::L; m < 32; m <<= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
-    }
-    if (lane < C::PAIRS) *reinterpret_cast<float2*>(&s_sum[warp_id() * D + runs.q[e >> 1] * 4 + 2 * (e & 1)]) = v;
+    const float2 v = make_float2(rows_sum<C::L>(sum[e].x), rows_sum<C::L>(sum[e].y));
+    if (lane < C::L) *reinterpret_cast<float2*>(&s_sum[warp_id() * D + runs.q[e >> 1] * 4 + 2 * (e & 1)]) = v;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += THREADS) {
