@@ -105,7 +105,10 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
   constexpr int TOKENS = rope::Cfg<D>::TOKENS, WARPS = rope::THREADS / 32;
   // Heads per unit and CTAs of q and of k: units go to warps in turn, so the slowest warp has
   // ceil(units / warps) of them, each worth its heads and about two more for its cosines.  Of all
-  // ways to cut the heads, the one whose slowest warp is the fastest.
+  // ways to cut the heads, the one whose slowest warp is the fastest.  The CTAs are shared out as if a
+  // unit cost four heads more: k's units have few heads, and a unit's first rows arrive with nothing
+  // else to do (12 + 3 heads of 256, 4 x 8192 tokens: 144 us with two, 136 with four; 24 + 6 heads of 128:
+  // 133 and 130; of 2 x 2305 tokens 27.5 and 28.9).
   const int64_t tgroups = (tokens + TOKENS - 1) / TOKENS;
   int64_t best = INT64_MAX;
   int ctas[2] = {1, 1};
@@ -118,7 +121,7 @@ fa_status rope_bwd_launch(RopeBwdParams& prm, bool inter, float* dwq, float* dwk
         chunks[k] = (prm.H[k] + most[k] - 1) / most[k];
         chunk[k] = (prm.H[k] + chunks[k] - 1) / chunks[k];
         units[k] = tgroups * chunks[k];
-        work[k] = units[k] * (chunk[k] + 2);
+        work[k] = units[k] * (chunk[k] + 4);
       }
       for (int k = 0; k < 2; ++k) {
         const int64_t share = int64_t(double(kRopeBwdCtas) * double(work[k]) / double(work[0] + work[1]) + 0.5);
