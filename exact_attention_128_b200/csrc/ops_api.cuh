@@ -194,9 +194,11 @@ int part_chunk(int64_t sets, int64_t blocks) {
 //     512 rows 77.6 / 32.5 us; 16384 tokens, 512 rows 249 / 55.6 us
 //   2 kv heads x 6, d = 128: 200 tokens, 384 rows 14.0 / 15.6 us, 768 rows 17.0 / 16.4 us
 //   8 kv heads x 4, d = 64: 200 tokens, 256 rows 12.4 / 16.3 us; 2000 tokens, 64 rows 15.0 / 13.8 us
-// Below 64 rows the two differ by less than the time it takes to call them up to some 2000 tokens.
-bool prefix_on_tensor_cores(int64_t rows, int64_t row_tiles, int Hkv, int d, int prefix_blocks) {
-  return rows >= 64 && row_tiles * Hkv * prefix_blocks >= (d == 64 ? 3000 : 640);
+//   8 requests of 32 heads, 8 kv heads, d = 128: 4000 tokens 27.5 / 17.4 us, 16384 tokens 51.8 / 28.4 us
+//   8 of 12 heads, 2 kv heads, d = 128, 2000 tokens: 14.3 / 12.4 us; 10 of 6 heads, 4000 tokens: 13.9 / 15.1 us
+//   14 of 32 heads, 8 kv heads, d = 64, 4371 tokens: 21.1 / 15.3 us
+bool prefix_on_tensor_cores(int64_t row_tiles, int Hkv, int d, int prefix_blocks) {
+  return row_tiles * Hkv * prefix_blocks >= (d == 64 ? 3000 : 640);
 }
 
 struct PartPlan {
@@ -211,7 +213,7 @@ PartPlan part_plan(int R, int Hq, int Hkv, int d, int max_blocks, int prefix_blo
   n.chunk = part_chunk(int64_t(R) * Hkv, max_blocks);
   n.own_parts = (max_blocks + n.chunk - 1) / n.chunk;
   const int64_t rows = int64_t(R) * G, row_tiles = (rows + part::ROWS - 1) / part::ROWS;
-  if (prefix_blocks > 0 && G <= part::ROWS && prefix_on_tensor_cores(rows, row_tiles, Hkv, d, prefix_blocks)) {
+  if (prefix_blocks > 0 && G <= part::ROWS && prefix_on_tensor_cores(row_tiles, Hkv, d, prefix_blocks)) {
     n.RT = 128 / G;
     n.pairs = (R + 2 * n.RT - 1) / (2 * n.RT);
     n.pre_parts = int((part::PREFIX_CTAS + int64_t(n.pairs) * Hkv - 1) / (int64_t(n.pairs) * Hkv)) + 1;

@@ -280,7 +280,7 @@ def decode_case(lens, Hq, Hkv, d, maxb, seed, prefix=0):
     return q, kc, vc, table, ptable, torch.tensor(lens, dtype=torch.int32)
 
 
-@pytest.mark.parametrize("wide", [0, 800])  # a much wider prefix table sends 64 rows and more to the tensor cores
+@pytest.mark.parametrize("wide", [0, 800])  # a much wider prefix table sends the prefix to the tensor cores
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize(
     "Hq,Hkv,prefix,lens",
