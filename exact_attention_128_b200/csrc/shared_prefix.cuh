@@ -13,7 +13,7 @@
 // device), and an item's tiles fall to a few consecutive CTAs, one partial result each.
 //   warp 0     producer of Q (by TMA, per item) and K: lane i < BN / 16 looks block i of a key tile
 //              up in the prefix table and issues its 16-row boxes; warp V_WARP the same for V.
-//   warp 1     MMA issuer: S_t = Q_t K^T into TMEM, then u_t += P_t V with P_t read from TMEM.
+//   warp 1     MMA issuer: S_t = Q_t K^T into TMEM, then u_t += P_t V with P_t (two parts) read from TMEM.
 //   warps 2-9  softmax of row tiles 0 and 1, one thread per row.
 // Scores are double-buffered in TMEM and issued one key tile ahead, so a softmax warp goes from
 // one tile to the next without waiting for its own P V (with one buffer, the chain S, softmax,
@@ -25,8 +25,10 @@
 // 830 TFLOP/s at the clocks of a short run; with the own tokens and the join 139 to 145 us power-capped.
 // BN = 64 and two K/V stages keep the CTA at 150 KB of shared memory and 352 threads of at most
 // 104 registers, so that a CTA of the requests' own (memory-bound) part runs on the SM beside it.
-// P is rounded to bf16 for P V: with many rows the tensor core is what bounds this part, and the
-// second product that would carry P's rest would cost it half as much again.
+// P is multiplied as the sum of two bf16 parts, its rounding and the rest, as in the pieces
+// (decode_part.cuh), so that a request's precision does not depend on its batch or its table: both
+// parts fit the 64 columns of the scores they come from.  The second product costs 256 requests behind
+// 16384 tokens 17 us (125 -> 142 us the step, the MMAs 14 of them), 8 behind 2000 tokens 0.6 us.
 #pragma once
 #include "decode_part.cuh"
 
@@ -232,8 +234,10 @@ __global__ void __maxnreg__(104)
     auto issue_PV = [&](int t, int st, int g, bool first) {
 #pragma unroll
       for (int ks = 0; ks < C::BN / 16; ++ks)
-        mma_ts_p(tmem + C::COL_O + t * D, tmem + (2 * (g & 1) + t) * C::BN + ks * 8,
-                 desc_add(dV, st * C::KV_TILE + ks * 16 * 128), idPV, (!first || ks > 0) ? 1u : 0u, leader);
+#pragma unroll
+        for (int half = 0; half < 2; ++half)  // P rounded, then the rest
+          mma_ts_p(tmem + C::COL_O + t * D, tmem + (2 * (g & 1) + t) * C::BN + half * (C::BN / 2) + ks * 8,
+                   desc_add(dV, st * C::KV_TILE + ks * 16 * 128), idPV, (!first || ks + half > 0) ? 1u : 0u, leader);
     };
     int kv = 0, local = 0;  // kv: K/V tiles so far, which is also the step (every tile is one)
     bool ok = true;
@@ -340,15 +344,19 @@ __global__ void __maxnreg__(104)
           float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < C::BN / 32; ++c) {
-            uint32_t pk[16];
+            uint32_t hi[16], lo[16];  // P = hi + lo, as in the pieces
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 y = __ffma2_rn(make_float2(f[c * 32 + 2 * i], f[c * 32 + 2 * i + 1]), sl2v, nbase);
               const float2 pv = make_float2(ex2(y.x), ex2(y.y));
               rs2[i & 3] = __fadd2_rn(rs2[i & 3], pv);
-              pk[i] = pack_bf16x2(pv.x, pv.y);
+              hi[i] = pack_bf16x2(pv.x, pv.y);
+              const float2 rest = __ffma2_rn(make_float2(__uint_as_float(hi[i] << 16), __uint_as_float(hi[i] & 0xffff0000u)),
+                                             make_float2(-1.f, -1.f), pv);
+              lo[i] = pack_bf16x2(rest.x, rest.y);
             }
-            tmem_st16(tS + c * 16, pk);
+            tmem_st16(tS + c * 16, hi);
+            tmem_st16(tS + C::BN / 2 + c * 16, lo);
           }
           const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
           l = l * alpha + (rsa.x + rsa.y);

@@ -361,7 +361,9 @@ size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int 
  *   block_table [R,max_blocks_per_seq] int32; prefix_len [1], ctx_lens [R] int32 (device).
  *   Either length may be 0, up to its table's capacity; a request with no token at all gets
  *   o = 0 and lse = -inf.  Table entries past a length's last block are never read.
- *   o [R,Hq,d] bf16, lse [R,Hq] fp32 or NULL (natural log).
+ *   o [R,Hq,d] bf16, lse [R,Hq] fp32 or NULL (natural log).  Weights enter the product with V to
+ *   2^-16, whatever the batch and the tables' widths (these choose between two kernels, whose
+ *   results may differ in the last bit of o).
  *   d in {64, 128}, block_size == 16, Hq / Hkv <= 16, dtype BF16; tables of up to 2^30 tokens (so
  *   in every call below, and in fa_qk_norm_rope_append).
  *   A length out of range or a bad block id is not dereferenced and sets the device status word

@@ -547,3 +547,28 @@ def test_gradients_of_broadcast_inputs():
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
     for a, b in zip(fa.qk_norm_rope(*wide, *args), fa.qk_norm_rope(*(t.contiguous() for t in wide), *args)):
         assert torch.equal(a, b)
+
+
+def own_and_prefix_bound(q, kc, vc, V, keys, d):
+    """Slack of o where P is carried as two bf16 parts everywhere: P off by 2 delta (scores) + 2^-22 (exponential) +
+    2^-16 (its second part rounded), relative; each 16 keys are added to a running sum of at most V = sum p |v| in
+    two products, which a tensor core may cut off below 2^-23 of it; the join adds 2^-20."""
+    delta, _ = bounds(q, kc, vc, d**-0.5)
+    return (2 * delta + 2.0**-22 + 2.0**-16 + keys / 16 * 2 * 2.0**-23 + 2.0**-20) * V
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,prefix,lens", [(12, 2, 40, (1,) * 8), (32, 8, 17, (0, 3) * 20), (4, 1, 300, (2,)),
+                                                (16, 2, 2000, (5,) * 70)])
+def test_shared_weights_are_not_rounded_to_bf16(d, Hq, Hkv, prefix, lens):
+    """The same bound on every way: 16-row pieces (a table of the prefix's width) and tensor cores (a wide one)."""
+    q, kc, vc, table, ptable, ctx = decode_case(lens, Hq, Hkv, d, 8, 660 + d + prefix, prefix)
+    O, L = ops.decode_shared(q, kc, vc, ptable, prefix, table, ctx, 16, d**-0.5)
+    V, _ = ops.decode_shared(q, kc, vc.abs(), ptable, prefix, table, ctx, 16, d**-0.5)
+    slack = own_and_prefix_bound(q, kc, vc, V, prefix + max(lens), d)
+    for wide in (0, 6000):
+        pt = torch.cat([ptable, torch.full((wide,), -1, dtype=torch.int32)])
+        o, _ = fa.paged_decode_shared(*(t.cuda() for t in (q, kc, vc, pt, torch.tensor([prefix], dtype=torch.int32),
+                                                           table, ctx)))
+        clean()
+        near(o, O, slack, f"o, {wide} blocks wider")
