@@ -187,18 +187,33 @@ int part_chunk(int64_t sets, int64_t blocks) {
 }
 
 // Whether the prefix goes to the tensor-core kernel, whose CTAs work on 256 rows at a time, or to
-// 16-row pieces, which read the prefix again for each 16 rows but need no kernel of their own and
-// keep P exact.  By the work, in (16 rows x block)s of the prefix's table; one step with 1 to 64 own
-// tokens, pieces against tensor cores:
-//   8 kv heads x 4, d = 128: 200 tokens, 128 rows 16.8 / 14.1 us; 2000 tokens, 64 rows 27.2 / 16.6 us,
-//     512 rows 77.6 / 32.5 us; 16384 tokens, 512 rows 249 / 55.6 us
-//   2 kv heads x 6, d = 128: 200 tokens, 384 rows 14.0 / 15.6 us, 768 rows 17.0 / 16.4 us
-//   8 kv heads x 4, d = 64: 200 tokens, 256 rows 12.4 / 16.3 us; 2000 tokens, 64 rows 15.0 / 13.8 us
-//   8 requests of 32 heads, 8 kv heads, d = 128: 4000 tokens 27.5 / 17.4 us, 16384 tokens 51.8 / 28.4 us
-//   8 of 12 heads, 2 kv heads, d = 128, 2000 tokens: 14.3 / 12.4 us; 10 of 6 heads, 4000 tokens: 13.9 / 15.1 us
-//   14 of 32 heads, 8 kv heads, d = 64, 4371 tokens: 21.1 / 15.3 us
-bool prefix_on_tensor_cores(int64_t row_tiles, int Hkv, int d, int prefix_blocks) {
-  return row_tiles * Hkv * prefix_blocks >= (d == 64 ? 3000 : 640);
+// 16-row pieces, which read the prefix again for each 16 rows but need no kernel of their own.  By
+// the rows of a kv head, the sets of 16 rows over all kv heads, the blocks of the prefix's table, and
+// the work, sets x blocks.  A step with 1 to 64 own tokens a request, replayed from a graph, pieces /
+// tensor cores in us (heads as query/kv; P tokens):
+//   d = 128, few rows: 1 request of 4/1, P 2000 8.8 / 11.3, 16384 12.7 / 18.0; 2 of 48/8 (12 rows), P 3000
+//     14.2 / 16.9, 32768 48.4 / 51.5
+//   one kv head, up to 4 sets: 4 of 4/1, P 300 11.7 / 10.7, 700 13.3 / 10.6, 4000 13.1 / 12.2, 16384 16.3 / 18.0; 16 of
+//     4/1, P 500 13.1 / 11.4, 6000 15.6 / 13.9
+//   60 to 128 blocks: 4 of 4/1, P 2000 12.8 / 11.3; 4 of 32/8, P 1000 13.4 / 12.1, 2000 15.0 / 14.1; 64 of
+//     8/2, P 1000 19.5 / 16.4; 8 of 12/2, P 2000 13.4 / 12.3
+//   more blocks, less than 4 sets or 2000 of work: 8 of 8/2, P 3000 13.6 / 14.7, 4000 13.7 / 15.1; 4 of 8/2,
+//     P 8000 14.6 / 16.3, 32768 20.1 / 23.0; 4 of 32/8, P 3000 15.7 / 17.6; but 8 of 8/2, P 6000 15.6 / 14.1
+//   more blocks, more work: 16 of 8/2, P 4000 18.8 / 15.8; 4 of 32/8, P 4000 18.7 / 17.5, 6000 19.1 / 19.8,
+//     16384 37.4 / 32.2; 64 of 32/8, P 16384 149 / 43.4
+//   fewer blocks: 64 of 8/2, P 300 14.5 / 20.9, 700 16.7 / 20.9; 200 of 8/1, P 300 19.3 / 22.2; 24 of 32/8, P 700
+//     20.0 / 17.6; 128 of 32/8, P 200 31.7 / 23.6; but 4 of 32/8, P 500 13.2 / 11.7; many
+//     sets: 256 of 32/8, P 40 41.1 / 33.4, 100 43.0 / 33.7
+//   d = 64 (pieces hold fewer registers): 4 of 32/8, P 32768 22.9 / 34.9; 16 of 8/2, P 8000 13.3 / 14.7; 8 of
+//     32/8, P 2000 11.6 / 12.3, 4000 15.1 / 14.9, 16384 25.6 / 23.4; 24 of 32/8, P 1000 14.4 / 13.0; 64 of 32/8,
+//     P 700 18.6 / 19.9, 2000 27.8 / 19.7, 16384 83.2 / 34.9; 64 of 8/2, P 3000 18.4 / 17.6; 256 of 32/8,
+//     P 100 24.2 / 21.8, 300 34.9 / 24.4
+bool prefix_on_tensor_cores(int64_t rows, int Hkv, int d, int blocks) {
+  const int64_t sets = (rows + part::ROWS - 1) / part::ROWS * Hkv, work = sets * blocks;
+  if (d == 64) return sets >= 512 || (sets >= 16 && work >= (blocks >= 60 ? 3000 : 8000));
+  if (rows < part::ROWS) return false;
+  if (Hkv == 1 && sets <= 4 && blocks >= 16 && blocks <= 400) return true;  // (no CTA works on two heads' tiles)
+  return (blocks >= 60 && blocks <= 128) || (sets >= 4 && work >= 2000) || sets >= 256;
 }
 
 struct PartPlan {
@@ -213,7 +228,7 @@ PartPlan part_plan(int R, int Hq, int Hkv, int d, int max_blocks, int prefix_blo
   n.chunk = part_chunk(int64_t(R) * Hkv, max_blocks);
   n.own_parts = (max_blocks + n.chunk - 1) / n.chunk;
   const int64_t rows = int64_t(R) * G, row_tiles = (rows + part::ROWS - 1) / part::ROWS;
-  if (prefix_blocks > 0 && G <= part::ROWS && prefix_on_tensor_cores(row_tiles, Hkv, d, prefix_blocks)) {
+  if (prefix_blocks > 0 && G <= part::ROWS && prefix_on_tensor_cores(rows, Hkv, d, prefix_blocks)) {
     n.RT = 128 / G;
     n.pairs = (R + 2 * n.RT - 1) / (2 * n.RT);
     n.pre_parts = int((part::PREFIX_CTAS + int64_t(n.pairs) * Hkv - 1) / (int64_t(n.pairs) * Hkv)) + 1;

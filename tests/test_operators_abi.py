@@ -177,3 +177,22 @@ def test_binding_rejects_cpu_tensors():
 def test_tables_of_more_than_2_30_tokens_are_refused(L, name, base, kw):
     """A kernel's token index plus its grid's stride stays inside 32 bits."""
     assert call(L, name, base, kw) == UNS
+
+
+def on_tensor_cores(L, R, Hq, Hkv, d, blocks):
+    """Which way a prefix goes, by the workspace: the tensor-core kernel leaves partial results of 256 rows a CTA."""
+    G = Hq // Hkv
+    items = -(-R // (2 * (128 // G))) * Hkv
+    tiles = items * (-(-148 // items) + 1) * 256 * (d + 1) * 4
+    pieces = R * Hq * (64 + 1) * (d + 1) * 4  # (a request's own 4 blocks are one piece)
+    assert tiles > 2 * pieces, "sizes at which the two cannot be told apart"
+    return L.fa_paged_decode_shared_workspace_size(R, Hq, Hkv, d, blocks, 4, 16) >= tiles
+
+
+@pytest.mark.parametrize("R,Hq,Hkv,d,blocks,want", [
+    (1, 4, 1, 128, 1024, False), (4, 4, 1, 128, 44, True), (1, 32, 8, 128, 125, False), (2, 16, 2, 128, 125, True), (4, 8, 2, 128, 500, False),
+    (10, 6, 2, 128, 250, False), (8, 12, 2, 128, 125, True), (8, 32, 8, 128, 1024, True), (4, 4, 1, 128, 2048, False),
+    (4, 32, 8, 64, 2048, False), (16, 8, 2, 64, 500, False), (8, 32, 8, 64, 1024, True)])
+def test_prefix_goes_the_faster_way(L, R, Hq, Hkv, d, blocks, want):
+    """Calls of few rows of which both ways were measured."""
+    assert on_tensor_cores(L, R, Hq, Hkv, d, blocks) == want
