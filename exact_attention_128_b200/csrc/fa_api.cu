@@ -3,6 +3,7 @@
 // this file only checks arguments and launches them on the caller's stream.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdio>
 #include <mutex>

@@ -266,14 +266,14 @@ bool part_sizes(int R, int Hq, int Hkv, int d, int max_blocks, int block_size) {
 
 template <int D>
 fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const PartParams& prm, const PartPlan& n,
-                        cudaStream_t st) {
+                        int withhold, cudaStream_t st) {
   using C = PrefixCfg<D>;
   CUtensorMap mq;
   const int G = prm.Hq / prm.Hkv;
   if (!make_map_rows(&mq, prm.q, D, prm.Hq, prm.R, G, n.RT)) return FA_ERR_CUDA;
   const PrefixParams pp{prm.pbt, prm.plen, const_cast<float*>(prm.pre_o), const_cast<float*>(prm.pre_lse), prm.R,
                         prm.Hkv, G, n.RT, n.pairs * prm.Hkv, n.pairs, n.pre_parts, prm.prefix_blocks, prm.num_blocks,
-                        prm.scale_log2, prm.wait_ns};
+                        prm.scale_log2, prm.wait_ns, withhold};
   // (all of the SM's memory as shared memory: the CTA of the next grid has to find room beside this one)
   static Prepared prepared;
   if (prepared.launch(fa_prefix_kernel<D>, dim3(part::PREFIX_CTAS), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, pp) !=
@@ -284,9 +284,9 @@ fa_status prefix_launch(const CUtensorMap& mk, const CUtensorMap& mv, const Part
 
 template <int D>
 fa_status part_run(const CUtensorMap& mk, const CUtensorMap& mv, PartParams& prm, const PartPlan& n, bool scored,
-                   cudaStream_t st) {
+                   int withhold, cudaStream_t st) {
   if (prm.pre_o) {
-    const fa_status s = prefix_launch<D>(mk, mv, prm, n, st);
+    const fa_status s = prefix_launch<D>(mk, mv, prm, n, withhold, st);
     if (s != FA_OK) return s;
     prm.late_wait = true;
   }
@@ -334,8 +334,9 @@ fa_status part_check(const void* q, const void* k_cache, const void* v_cache, co
 fa_status part_call(const void* q, const void* k_cache, const void* v_cache, const int* prefix_table,
                     const int* prefix_len, const int* block_table, const int* ctx_lens, float* weights, void* o,
                     float* lse, int R, int Hq, int Hkv, int d, int max_prefix_blocks, int max_blocks, int num_blocks,
-                    float scale, void* workspace, size_t workspace_bytes, void* stream) {
+                    float scale, void* workspace, size_t workspace_bytes, void* stream, int withhold = INT_MAX) {
   const PartPlan n = part_plan(R, Hq, Hkv, d, max_blocks, max_prefix_blocks, weights != nullptr);
+  if (withhold != INT_MAX && n.pairs == 0) return FA_ERR_UNSUPPORTED;  // (the self-test is the tensor-core kernel's)
   if (!workspace || workspace_bytes < n.bytes || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   PartParams prm{static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(o), lse,
@@ -350,8 +351,23 @@ fa_status part_call(const void* q, const void* k_cache, const void* v_cache, con
   const long cache_rows = long(num_blocks) * Hkv * part::BS;
   if (!make_map_cache(&mk, k_cache, cache_rows, d) || !make_map_cache(&mv, v_cache, cache_rows, d)) return FA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 64 ? part_run<64>(mk, mv, prm, n, weights != nullptr, st)
-                 : part_run<128>(mk, mv, prm, n, weights != nullptr, st);
+  return d == 64 ? part_run<64>(mk, mv, prm, n, weights != nullptr, withhold, st)
+                 : part_run<128>(mk, mv, prm, n, weights != nullptr, withhold, st);
+}
+
+fa_status shared_call(const fa_paged_decode_shared_args* args, int withhold, void* stream) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  const fa_paged_decode_shared_args& a = *args;
+  if (!a.prefix_table || !a.prefix_len || a.max_prefix_blocks <= 0 || !aligned(a.prefix_table, 4) ||
+      !aligned(a.prefix_len, 4))
+    return FA_ERR_INVALID_ARG;
+  const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
+                                 a.d, a.block_size, a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
+  if (s != FA_OK) return s;
+  if (int64_t(a.max_prefix_blocks) * part::BS > kMaxTokens) return FA_ERR_UNSUPPORTED;
+  return part_call(a.q, a.k_cache, a.v_cache, a.prefix_table, a.prefix_len, a.block_table, a.ctx_lens, nullptr, a.o,
+                   a.lse, a.R, a.Hq, a.Hkv, a.d, a.max_prefix_blocks, a.max_blocks_per_seq, a.num_blocks, a.scale,
+                   a.workspace, a.workspace_bytes, stream, withhold);
 }
 
 struct EvictPlan {
@@ -500,18 +516,11 @@ size_t fa_paged_decode_shared_workspace_size(int R, int Hq, int Hkv, int d, int 
 }
 
 fa_status fa_paged_decode_shared(const fa_paged_decode_shared_args* args, void* stream) {
-  if (!args) return FA_ERR_INVALID_ARG;
-  const fa_paged_decode_shared_args& a = *args;
-  if (!a.prefix_table || !a.prefix_len || a.max_prefix_blocks <= 0 || !aligned(a.prefix_table, 4) ||
-      !aligned(a.prefix_len, 4))
-    return FA_ERR_INVALID_ARG;
-  const fa_status s = part_check(a.q, a.k_cache, a.v_cache, a.block_table, a.ctx_lens, a.o, a.lse, a.R, a.Hq, a.Hkv,
-                                 a.d, a.block_size, a.max_blocks_per_seq, a.num_blocks, a.scale, a.dtype);
-  if (s != FA_OK) return s;
-  if (int64_t(a.max_prefix_blocks) * part::BS > kMaxTokens) return FA_ERR_UNSUPPORTED;
-  return part_call(a.q, a.k_cache, a.v_cache, a.prefix_table, a.prefix_len, a.block_table, a.ctx_lens, nullptr, a.o,
-                   a.lse, a.R, a.Hq, a.Hkv, a.d, a.max_prefix_blocks, a.max_blocks_per_seq, a.num_blocks, a.scale,
-                   a.workspace, a.workspace_bytes, stream);
+  return shared_call(args, INT_MAX, stream);
+}
+
+fa_status fa_selftest_shared_timeout(const fa_paged_decode_shared_args* args, int tiles, void* stream) {
+  return tiles < 0 ? FA_ERR_INVALID_ARG : shared_call(args, tiles, stream);
 }
 
 size_t fa_paged_decode_scored_workspace_size(int R, int Hq, int Hkv, int d, int max_blocks_per_seq, int block_size) {

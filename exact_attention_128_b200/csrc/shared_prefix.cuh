@@ -78,6 +78,7 @@ struct PrefixParams {
   int prefix_blocks, num_blocks;
   float scale_log2;
   uint64_t wait_ns;
+  int withhold;  // K tiles that a CTA loads at most (the self-test's; INT_MAX otherwise)
 };
 
 struct PrefixBars {
@@ -175,6 +176,10 @@ __global__ void __maxnreg__(104)
         }
       }
       for (int j = j0; j < j1; ++j, ++kv) {
+        if (!is_v && kv >= p.withhold) {
+          ok = false;
+          break;
+        }
         const int st = kv % C::NSTAGE, round = kv / C::NSTAGE;
         const int lb = j * NB + lane;
         const int ph_next = (lane < NB && j + 1 < j1 && lb + NB < nblk) ? __ldg(p.pbt + lb + NB) : 0;
@@ -414,6 +419,15 @@ __global__ void __maxnreg__(104)
         }
       }
       p.part_lse[row0 + lane] = m + __log2f(l);
+    }
+    if (!ok) {  // NaN for the item in progress and those behind it, so that nothing merged from them looks valid
+      int i = 0;
+      for (long long x = x0; x < x1; ++i) {
+        const int it = int(x / deal.nt);
+        x = min(x1, (long long)(it + 1) * deal.nt);
+        const int part = int(blockIdx.x) - deal.owner((long long)(it)*deal.nt);
+        if (i >= local) p.part_lse[((size_t(it) * p.parts + part) * 2 + t) * C::BM + wq * 32 + lane] = NAN;
+      }
     }
   }
   tc_fence_before();

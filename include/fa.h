@@ -474,6 +474,14 @@ void fa_set_wait_limit_ns(uint64_t ns);
  */
 fa_status fa_selftest_wait_timeout(void* stream);
 
+/*
+ * fa_selftest_shared_timeout — fa_paged_decode_shared, whose prefix kernel loads no more than `tiles`
+ * (>= 0) of a CTA's key tiles, so that the wait for the next one runs out after the current limit: the
+ * rows behind it get NaN in o and lse, and the device status word FA_ERR_DEVICE_TIMEOUT.  For tests of
+ * the timeout path, as above; FA_ERR_UNSUPPORTED for sizes that do not go to that kernel.
+ */
+fa_status fa_selftest_shared_timeout(const fa_paged_decode_shared_args* args, int tiles, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

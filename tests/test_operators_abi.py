@@ -196,3 +196,11 @@ def on_tensor_cores(L, R, Hq, Hkv, d, blocks):
 def test_prefix_goes_the_faster_way(L, R, Hq, Hkv, d, blocks, want):
     """Calls of few rows of which both ways were measured."""
     assert on_tensor_cores(L, R, Hq, Hkv, d, blocks) == want
+
+
+def test_the_timeout_self_test_takes_sizes_of_the_tensor_core_kernel(L):
+    pack = lambda **kw: PACKED["fa_paged_decode_shared"].pack(*(0 if v is None else v for v in {**SHARED, **kw}.values()))
+    assert L.fa_selftest_shared_timeout(None, 1, None) == BAD
+    assert L.fa_selftest_shared_timeout(pack(R=64, pb=128), -1, None) == BAD
+    assert L.fa_selftest_shared_timeout(pack(R=64, pb=128, o=None), 1, None) == BAD
+    assert L.fa_selftest_shared_timeout(pack(R=1, pb=8), 1, None) == UNS

@@ -572,3 +572,37 @@ def test_shared_weights_are_not_rounded_to_bf16(d, Hq, Hkv, prefix, lens):
                                                            table, ctx)))
         clean()
         near(o, O, slack, f"o, {wide} blocks wider")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,R,prefix,tiles", [(12, 2, 90, 900, 0), (16, 4, 70, 2500, 1), (32, 8, 300, 4000, 2)])
+def test_a_prefix_wait_that_ran_out_leaves_nan(d, Hq, Hkv, R, prefix, tiles):
+    """Key tiles that never come: no row shows what the workspace held before, and the next call is unharmed."""
+    import struct
+
+    blocks, maxb = 4096, 2  # (a wide table, so that the prefix goes to the kernel whose waits are meant)
+    g = torch.Generator().manual_seed(R)
+    used = -(-prefix // 16)
+    ids = torch.randperm(used + R * maxb, generator=g).int()
+    pt = torch.full((blocks,), -1, dtype=torch.int32)
+    pt[:used] = ids[:used]
+    kc, vc = (randn((used + R * maxb, Hkv, 16, d), 670 + i, BF).cuda() for i in (0, 1))
+    q, table = randn((R, Hq, d), 672, BF).cuda(), ids[used:].view(R, maxb).cuda()
+    ctx = torch.randint(0, 33, (R,), generator=g).int().cuda()
+    pt, pl = pt.cuda(), torch.tensor([prefix], dtype=torch.int32).cuda()
+    need = fa.paged_decode_shared_workspace_size(R, Hq, Hkv, d, blocks, maxb, 16)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    args = (q, kc, vc, pt, pl, table, ctx)
+    o, lse = fa.paged_decode_shared(*args, workspace=ws)
+    clean()
+    assert torch.isfinite(lse).all()
+    o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+    at = [t.data_ptr() for t in (q, kc, vc, pt, pl, table, ctx, o2, lse2, ws)]
+    packed = struct.pack("11P8ifi", *at, need, R, Hq, Hkv, d, 16, blocks, maxb, kc.shape[0], d**-0.5, fa.FA_DTYPE_BF16)
+    fa.device_status(reset=True)
+    assert fa.lib().fa_selftest_shared_timeout(packed, tiles, torch.cuda.current_stream().cuda_stream) == fa.FA_OK
+    assert fa.device_status(reset=True) == fa.FA_ERR_DEVICE_TIMEOUT
+    assert torch.isnan(lse2).all() and torch.isnan(o2).all()
+    o3, lse3 = fa.paged_decode_shared(*args, workspace=ws)
+    clean()
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
