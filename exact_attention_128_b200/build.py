@@ -8,6 +8,7 @@ compiled against the installed torch); it links neither the library nor a kernel
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -76,9 +77,17 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    build_binding(force)
-    if not force and up_to_date():
-        return LIB
+    """The library, which needs nvcc alone, and then the binding (left out on a host without torch)."""
+    if force or not up_to_date():
+        build_library(verbose, extra_flags)
+    if importlib.util.find_spec("torch"):
+        build_binding(force)
+    else:
+        print("torch is not installed: _binding.so, the Python side of some calls, is not built", file=sys.stderr)
+    return LIB
+
+
+def build_library(verbose: bool = False, extra_flags=()) -> str:
     cmd = [
         nvcc_path(),
         *ARCH,
