@@ -117,7 +117,7 @@ __device__ __forceinline__ void evict_move_rows(const EvictParams& p, const int*
 
 __global__ void __launch_bounds__(evict::THREADS) fa_evict_select_kernel(const __grid_constant__ EvictParams p) {
   using namespace evict;
-  extern __shared__ uint32_t evict_smem[];
+  extern __shared__ __align__(16) uint32_t evict_smem[];
   __shared__ __align__(16) int s_hist[BINS];
   __shared__ int4 s_warp[THREADS / 128];
   __shared__ int s_found[3];  // the digit's bin, how many of its tokens are needed, and how many it has

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
   constexpr bool SPREAD = sizeof(T) + sizeof(TG) + sizeof(TO) > 6;  // any of them fp32
   using RX = Slot<T, SPREAD>;
   using RG = Slot<TG, SPREAD>;
-  extern __shared__ uint8_t rope_smem[];
+  extern __shared__ __align__(16) uint8_t rope_smem[];
   const uint32_t slot_x = smem_u32(rope_smem) + RG::BYTES + threadIdx.x * RX::PIECE;
   const uint32_t slot_g = smem_u32(rope_smem) + threadIdx.x * RG::PIECE;
   const int kind = int(blockIdx.x) < p.ctas_q ? 0 : 1;

@@ -204,3 +204,22 @@ def test_the_timeout_self_test_takes_sizes_of_the_tensor_core_kernel(L):
     assert L.fa_selftest_shared_timeout(pack(R=64, pb=128), -1, None) == BAD
     assert L.fa_selftest_shared_timeout(pack(R=64, pb=128, o=None), 1, None) == BAD
     assert L.fa_selftest_shared_timeout(pack(R=1, pb=8), 1, None) == UNS
+
+
+def test_dynamic_shared_memory_is_aligned():
+    """16-byte accesses need it: every dynamic array says so, or its kernel rounds (or checks) the address itself."""
+    import glob
+    import os
+    import re
+
+    csrc = os.path.join(os.path.dirname(os.path.abspath(fa.__file__)), "csrc")
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu*"))):
+        lines = open(path).read().splitlines()
+        for i, line in enumerate(lines):
+            if "extern __shared__" not in line:
+                continue
+            seen += 1
+            aligned = re.search(r"__align__\((16|128|1024)\)", line) or "1023" in "".join(lines[i + 1 : i + 3])
+            assert aligned, f"{os.path.basename(path)}:{i + 1}: {line.strip()}"
+    assert seen >= 10
