@@ -214,10 +214,12 @@ __global__ void __launch_bounds__(dec::WARPS * 32)
     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    const float n0 = fmaxf(m0, mx0 * sl2), n1 = fmaxf(m1, mx1 * sl2);  // every block has a cached token
-    const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1);                  // 0 on the first block
-    m0 = n0;
-    m1 = n1;
+    const float old0 = m0, old1 = m1;
+    m0 = fmaxf(m0, mx0 * sl2);
+    m1 = fmaxf(m1, mx1 * sl2);
+    // (scores of -inf alone so far, from keys with infinities: their mass is 0)
+    const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
+    const float a0 = ex2(old0 - n0), a1 = ex2(old1 - n1);  // 0 on the first block
     float pr[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(dec::WARPS * 32)
       if (d == 0 && p.lse) p.lse[size_t(r) * p.Hq + h] = lse_nat;
     } else {
       const size_t pi = (size_t(r) * p.Hq + h) * p.max_splits + s;
-      p.part_o[pi * D + d] = U / L;
+      p.part_o[pi * D + d] = L == 0.f ? 0.f : U / L;  // (a split without mass: lse = -inf, no share in the row)
       if (d == 0) p.part_lse[pi] = lse_nat;
     }
   }

@@ -606,3 +606,21 @@ def test_a_prefix_wait_that_ran_out_leaves_nan(d, Hq, Hkv, R, prefix, tiles):
     o3, lse3 = fa.paged_decode_shared(*args, workspace=ws)
     clean()
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+@pytest.mark.parametrize("dead", [1, 16, 64, 700, 2048, 2100])
+def test_paged_decode_scores_of_minus_infinity(dead):
+    """The decode step without weights, too: keys without mass in a block, in each warp's first, in a whole split."""
+    lens = (2200, 2101, 4200)
+    q, kc, vc, table, _, ctx = decode_case(lens, 8, 2, 128, 270, 760 + dead)
+    rows = [(table[r, b], slice(0, min(16, dead - 16 * b))) for r in range(3) for b in range(-(-dead // 16))]
+    finite = minus_infinity(q, kc, rows)
+    o, lse = fa.paged_decode(*(t.cuda() for t in (q, kc, vc, table, ctx)))
+    clean()
+    O, L = ora.paged_decode(q, kc, vc, table, ctx, 16, 128**-0.5)
+    assert np.isfinite(O).all() and np.isfinite(L).all()
+    delta, slack = bounds(q, finite, vc, 128**-0.5)
+    V, _ = ora.paged_decode(q, kc, vc.abs(), table, ctx, 16, 128**-0.5)
+    near(o, O, slack + 2.0**-8 * V, "o")  # (this call rounds P to bf16 once)
+    # the log-sum goes from base 2 to e and through the splits' merge: a rounding and a function's 2^-21 each
+    near(lse, L, delta + 2.0**-20 * (np.abs(L) + 1), "lse")
