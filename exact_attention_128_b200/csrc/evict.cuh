@@ -16,8 +16,8 @@
 // one copy of an 11-bit digit the selection of 8192 tokens took 32 us, most of it there).  Which
 // tokens are above the threshold, and which equal it, become bit masks of 32 tokens; prefix sums of
 // their population counts give every freed slot and every moving token its number.
-// The CTA then moves the rows itself, or, where there are too few CTAs for the moves to fill the
-// device, a second kernel does.
+// The CTA then moves the rows itself, or, where min(keep, the table's tokens - keep) rows may be too many
+// for that, a second kernel does (evict_plan in ops_api.cuh, with both sides measured).
 //
 // What bounds it: after long prompts, the rows that move (32 requests x 8 heads of 4097 to 8192 tokens,
 // keep 2048: 22 us of selection, then 66 us for about 390 MB of rows read and written, 5.9 TB/s); in

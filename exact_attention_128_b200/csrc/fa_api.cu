@@ -108,9 +108,14 @@ cudaError_t set_smem(K kernel, int bytes) {
 fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // Launch `kernel` as a programmatic dependent on stream st: it may be launched while the
-// grid before it is still finishing.  Every kernel launched this way executes
-// griddepcontrol.wait before its first global access, which returns once that grid has
-// completed and its writes are visible.
+// grid before it is still finishing.  Kernels launched this way execute griddepcontrol.wait,
+// which returns once that grid has completed and its writes are visible, before they read
+// anything that it may have written and before their first write.  Where a kernel reads
+// something earlier (the join of the decode over pieces: lengths and old weights), or waits in one
+// CTA alone (its own-part grid behind the prefix kernel), this rests on the grid before it: every
+// CTA of that one triggers (griddepcontrol.launch_dependents) only behind its own wait, so that all
+// earlier grids are done by then, and it writes nothing that is read early.  A trigger in front of
+// the wait in either of those kernels would break it.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args&&... args) {
