@@ -381,9 +381,15 @@ EvictPlan evict_plan(int R, int Hkv, int max_blocks, int keep) {
   const int64_t M = int64_t(max_blocks) * evict::BS, sets = int64_t(R) * Hkv;
   n.cap = int(std::max<int64_t>(0, std::min<int64_t>(keep, M - keep)));
   n.in_smem = M <= evict::MAX_KEYS;
-  // The selecting CTAs move the rows themselves where there are few, which saves a launch.  Many
-  // rows go to a second kernel, which spreads them evenly: 32 requests x 8 heads of 4097 to 8192
-  // tokens, kept 2048, moved in 67 us, while 256 CTAs on 148 SMs took 75 us.
+  // The selecting CTAs move the rows themselves where few can move, which saves a launch.  Many
+  // rows go to a second kernel, which spreads them evenly.  A call replayed from a graph, itself / second, us:
+  //   128 rows move, sets of (request, kv head) 2, 64, 256, 512: 5.9 / 7.5, 8.9 / 10.8, 12.2 / 14.5, 21.9 / 24.6
+  //   480 of 4096: 12.8 / 10.6, 14.9 / 14.3, 33.4 / 33.6, 67.0 / 65.7;  512 of 1024: 10.3 / 9.6, 10.7 / 10.8, 17.1 / 19.4,
+  //     44.7 / 45.6
+  //   750 of 1500: 12.2 / 9.6, 12.5 / 12.1, 29.2 / 29.2, 60.2 / 58.1 (128 sets 13.0 / 14.8)
+  //   2048 of 4097 to 8192: 23.0 / 12.8, 42.2 / 29.1, 97.4 / 85.9, 180 / 169
+  // The lengths are on the device, so the table's width decides: in one of 8192 tokens, steady contexts
+  // of 2049 to 2176 with 2048 kept take the second kernel: 7.3 / 8.8, 9.6 / 11.2, 13.7 / 15.1, 24.9 / 27.3.
   n.fused = n.in_smem && n.cap <= 512;
   n.off_moves = n.fused ? 0 : align256(size_t(sets) * sizeof(int));
   n.off_masks = n.off_moves + (n.fused ? 0 : align256(size_t(sets) * 2 * n.cap * sizeof(int)));

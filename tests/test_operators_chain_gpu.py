@@ -349,3 +349,48 @@ def test_threads_call_at_once():
     for i in range(len(cases)):
         assert all(torch.equal(a, b) for a, b in zip(got[i], (*ref[i], *kept[i])))
     assert fa.device_status() == 0
+
+
+@pytest.mark.parametrize("keep,recent", [(32, 12), (17, 0), (48, 48)])
+def test_evictions_in_a_loop_keep_whole_tokens(keep, recent):
+    """After each eviction: the lengths are min(before, keep), every live slot names its token, once, and holds that
+    token's key, value and weight, whatever was evicted before."""
+    s = Server(maxb=6)
+    R, Hkv, d = s.R, s.Hkv, s.d
+    lens = torch.tensor([50, 7, 31], device="cuda", dtype=torch.int32)
+    s.token(randn((R, 50, 10, d), 130, BF).cuda(), lens)
+    one = torch.ones(R, device="cuda", dtype=torch.int32)
+
+    def rows():
+        """{position: (key, value, weight)} of every (request, head)."""
+        kc, vc, w, sp, table = (t.cpu() for t in (s.kc, s.vc, s.w, s.sp, s.table))
+        out = {}
+        for r, (n, seq) in enumerate(zip(s.ctx.tolist(), s.seq.tolist())):
+            for h in range(Hkv):
+                out[r, h] = {}
+                for slot in range(n):
+                    p = int(sp[r, h, slot]) if sp[r, h, slot] >= 0 else seq - n + slot
+                    b, i = table[r, slot // 16], slot % 16
+                    out[r, h][p] = (kc[b, h, i], vc[b, h, i], w[r, h, slot])
+                assert len(out[r, h]) == n
+        return out
+
+    for t in range(24):
+        s.step(randn((R, 1, 10, d), 140 + t, BF).cuda(), one)
+        if t % 8 != 7:
+            continue
+        before, was = rows(), s.ctx.tolist()
+        s.evict(keep, recent)
+        assert s.ctx.tolist() == [min(n, keep) for n in was]
+        after = rows()
+        for (r, h), now in after.items():
+            n, seq = int(s.ctx[r]), int(s.seq[r])
+            assert (s.sp[r, h, :n] >= 0).all() and (s.sp[r, h, n:] == -1).all() and (s.w[r, h, n:] == 0).all()
+            for p, (k, v, w) in now.items():
+                assert torch.equal(k, before[r, h][p][0]) and torch.equal(v, before[r, h][p][1]) and w == before[r, h][p][2]
+            newest = {p for p in before[r, h] if p >= seq - recent}
+            assert newest <= set(now)
+            dropped = [float(x[2]) for p, x in before[r, h].items() if p not in now]
+            heavy = [float(x[2]) for p, x in now.items() if p < seq - recent]
+            assert not dropped or not heavy or max(dropped) <= min(heavy)
+    assert fa.device_status() == 0
