@@ -22,8 +22,9 @@
 // TB/s, and 4 us for the weights' sums.
 //
 // Angles: the position (up to 2^31) times the frequency is taken in turns in 64 bits and reduced
-// to [-1/2, 1/2] before it is rounded to 32 bits, so far positions lose nothing; no table of
-// cosines is read.  All arithmetic behind that is fp32 with one rounding at the end.
+// to [-1/2, 1/2] before it is rounded to 32 bits, so far positions lose nothing (and where the results
+// have 32 bits, the rounded part is not lost either); no table of cosines is read.  All arithmetic
+// behind that is fp32 with one rounding at the end.
 #pragma once
 #include "common.cuh"
 
@@ -198,9 +199,29 @@ __device__ __forceinline__ void rows_wait() {  // all but this thread's newest N
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Cosine and sine of a position times a frequency.  FINE (results of 32 bits): what the reduced angle
+// loses when it is rounded, up to 2^-26 turns, is added back (the first term of the series); for a result
+// of 16 bits it does not matter.
+template <bool FINE>
+__device__ __forceinline__ void turn_of(int pos, double freq, float& s, float& c) {
+  const double turns = double(pos) * (freq * 0.15915494309189533577), part = turns - rint(turns);
+  const float near = float(part);
+  sincospif(2.f * near, &s, &c);
+  if constexpr (FINE) {
+    const float rest = float(part - double(near)) * 6.2831853f, s0 = s;
+    s = fmaf(c, rest, s);
+    c = fmaf(-s0, rest, c);
+  }
+}
+// 1 / sqrt(v), for results of 32 bits rounded to the nearest (rsqrtf is off by up to two steps).
+template <bool FINE>
+__device__ __forceinline__ float inverse_root(float v) {
+  return FINE ? __frsqrt_rn(v) : rsqrtf(v);
+}
+
 // Cosines and sines of a lane's 8 pairs for one token (lanes behind the rotary width: 1 and 0).
 // `pos` points at the token's position on axis 0.
-template <bool INTER, int D, bool SPREAD>
+template <bool INTER, bool FINE, int D, bool SPREAD>
 __device__ __forceinline__ void angles(const Runs<D, SPREAD>& r, const int* pos, int64_t pos_sa, const double* freq,
                                        int rd, int sec0, int sec1, float2 (&cs)[4], float2 (&sn)[4]) {
   const bool turns_at_all = r.q[0] * 4 < rd;
@@ -211,8 +232,7 @@ __device__ __forceinline__ void angles(const Runs<D, SPREAD>& r, const int* pos,
       // pair e: adjacent values of run e / 2, or value e % 4 of run e / 4 with its partner
       const int f = INTER ? r.q[e >> 1] * 2 + (e & 1) : r.q[e >> 2] * 4 + (e & 3);
       const int axis = f < sec0 ? 0 : f < sec1 ? 1 : 2;
-      const double turns = double(__ldg(pos + axis * pos_sa)) * (__ldg(freq + f) * 0.15915494309189533577);
-      sincospif(2.f * float(turns - rint(turns)), &s, &c);
+      turn_of<FINE>(__ldg(pos + axis * pos_sa), __ldg(freq + f), s, c);
     }
     (e & 1 ? sn[e >> 1].y : sn[e >> 1].x) = s;
     (e & 1 ? cs[e >> 1].y : cs[e >> 1].x) = c;
@@ -231,8 +251,7 @@ __device__ __forceinline__ void table_entry(float4* table, int lane, int e, cons
   if (on && r.q[0] * 4 < rd) {
     const int f = INTER ? r.q[e >> 1] * 2 + (e & 1) : r.q[e >> 2] * 4 + (e & 3);
     const int axis = f < sec0 ? 0 : f < sec1 ? 1 : 2;
-    const double turns = double(__ldg(pos + axis * pos_sa)) * (__ldg(freq + f) * 0.15915494309189533577);
-    sincospif(2.f * float(turns - rint(turns)), &s, &c);
+    turn_of<SPREAD>(__ldg(pos + axis * pos_sa), __ldg(freq + f), s, c);  // (forward: spread rows are fp32 ones)
   }
   float* at = reinterpret_cast<float*>(table + (e >> 2) * 32 + lane) + (e & 3);
   at[0] = c;
@@ -319,7 +338,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
     fa_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
   using namespace rope;
   using C = Cfg<D>;
-  constexpr bool SPREAD = sizeof(T) == 4;
+  constexpr bool SPREAD = sizeof(T) == 4, FINE = SPREAD;
   constexpr int STAGES = SPREAD ? FWD_STAGES_F32 : FWD_STAGES;
   using R = Slot<T, SPREAD>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
@@ -408,7 +427,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::FWD_CTAS)
         float2 sq = mul2(f[0], f[0]);
 #pragma unroll
         for (int e = 1; e < 8; ++e) sq = fma2(f[e], f[e], sq);
-        const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
+        const float2 r = both(inverse_root<FINE>(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
         float2 w[8];
         read_planes(s_w + kind * 4 * C::L + c, C::L, w);
 #pragma unroll
@@ -441,6 +460,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
   using namespace rope;
   using C = Cfg<D>;
   constexpr bool SPREAD = sizeof(T) + sizeof(TG) + sizeof(TO) > 6;  // any of them fp32
+  constexpr bool FINE = sizeof(TO) == 4;
   using RX = Slot<T, SPREAD>;
   using RG = Slot<TG, SPREAD>;
   extern __shared__ __align__(16) uint8_t rope_smem[];
@@ -486,7 +506,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
     for (int i = 0; i < BWD_STAGES - 1; ++i) fetch(i);
     float2 cs[4], sn[4];
     if (on) {
-      angles<INTER>(runs, p.pos + b * p.pos_sb + n, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, cs, sn);
+      angles<INTER, FINE>(runs, p.pos + b * p.pos_sb + n, p.pos_sa, p.freq, p.rd, p.sec0, p.sec1, cs, sn);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sn[e] = neg2(sn[e]);
     }
@@ -503,7 +523,7 @@ __global__ void __launch_bounds__(rope::THREADS, rope::BWD_CTAS)
         float2 sq = mul2(xn[0], xn[0]);
 #pragma unroll
         for (int e = 1; e < 8; ++e) sq = fma2(xn[e], xn[e], sq);
-        const float2 r = both(rsqrtf(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
+        const float2 r = both(inverse_root<FINE>(row_sum<C::L>(sq.x + sq.y) * (1.f / D) + p.eps));
         float2 dot2 = both(0.f);
         if (on) {
 #pragma unroll

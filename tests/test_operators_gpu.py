@@ -624,3 +624,39 @@ def test_paged_decode_scores_of_minus_infinity(dead):
     near(o, O, slack + 2.0**-8 * V, "o")  # (this call rounds P to bf16 once)
     # the log-sum goes from base 2 to e and through the splits' merge: a rounding and a function's 2^-21 each
     near(lse, L, delta + 2.0**-20 * (np.abs(L) + 1), "lse")
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_fp32_rotation_rounds_no_more_than_the_plain_form(norm, inter):
+    """fp32 rows against 64 bits: the mean square error is at most that of the plain form, whose angles, cosines and
+    roots are right to the last bit (it rounds three products and a sum to a value, the kernel two and a sum)."""
+    q, k, _, (wq, wk), pos, freq = rope_inputs(4, 6, 2, 700, 128, 128, (64,), F32, norm, 60)
+    dqo, dko = (randn(t.shape, 61 + i, F32).cuda() for i, t in enumerate((q, k)))
+    got = fa.qk_norm_rope(q, k, wq, wk, pos, freq, interleaved=inter)
+    grads = fa.qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, freq, interleaved=inter)[:2]
+    clean()
+
+    def plain(x, dy, w, dtype):
+        t = (pos[0].double()[:, None, :, None] * freq)
+        c, s = t.cos().to(dtype), t.sin().to(dtype)
+        i = torch.arange(64, device="cuda")
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + 64)
+
+        def turn(y, s):
+            out = torch.empty_like(y)
+            out[..., a], out[..., b] = y[..., a] * c - y[..., b] * s, y[..., a] * s + y[..., b] * c
+            return out
+
+        x, dy = x.to(dtype), dy.to(dtype)
+        g = turn(dy, -s)
+        if w is None:
+            return turn(x, s), g
+        r = 1 / (x.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+        h = g * w.to(dtype)
+        return turn(x * r * w.to(dtype), s), r * (h - x * r * (h * (x * r)).mean(-1, keepdim=True))
+
+    for j, (x, dy, w) in enumerate(((q, dqo, wq), (k, dko, wk))):
+        for mine, p32, p64 in zip((got[j], grads[j]), plain(x, dy, w, F32), plain(x, dy, w, torch.float64)):
+            mine, p32 = ((v.double() - p64).square().mean().sqrt().item() for v in (mine, p32))
+            assert mine <= p32, (mine, p32)
