@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <mutex>
 #include <utility>
+#include <utility>
 
 #include "common.cuh"
 #include "decode.cuh"

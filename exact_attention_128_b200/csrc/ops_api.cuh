@@ -74,6 +74,20 @@ bool rope_rows(const void* p, const int64_t* strides, int dtype) {
   return true;
 }
 
+// Whether rows of d values at these strides may share memory: each dimension's step has to clear all that the
+// dimensions of smaller steps cover, as in any permuted slice of a dense array.
+bool rows_overlap(const int64_t* strides, int B, int H, int N, int d) {
+  std::pair<int64_t, int> dims[3] = {{strides[0], B}, {strides[1], H}, {strides[2], N}};
+  std::sort(dims, dims + 3);
+  __int128 covered = d;
+  for (const auto& [step, n] : dims) {
+    if (n <= 1) continue;
+    if (step < covered) return true;
+    covered += __int128(step) * (n - 1);
+  }
+  return false;
+}
+
 template <typename T, int D, bool PAGED>
 fa_status rope_launch(RopeParams& prm, bool inter, cudaStream_t st) {
   const int64_t tokens = int64_t(prm.B) * prm.N;
@@ -479,11 +493,8 @@ fa_status fa_qk_norm_rope_bwd(const fa_qk_norm_rope_bwd_args* args, void* stream
   if (!rope_rows(a.q, a.q_strides, a.dtype) || !rope_rows(a.k, a.k_strides, a.dtype) ||
       !rope_rows(a.dq, a.dq_strides, a.grad_dtype) || !rope_rows(a.dk, a.dk_strides, a.grad_dtype))
     return FA_ERR_INVALID_ARG;
-  // no two rows of a gradient may share memory
-  const int n[2][3] = {{a.B, a.Hq, a.N}, {a.B, a.Hkv, a.N}};
-  for (int t = 0; t < 2; ++t)
-    for (int i = 0; i < 3; ++i)
-      if (n[t][i] > 1 && (t ? a.dk_strides : a.dq_strides)[i] < a.d) return FA_ERR_INVALID_ARG;
+  if (rows_overlap(a.dq_strides, a.B, a.Hq, a.N, a.d) || rows_overlap(a.dk_strides, a.B, a.Hkv, a.N, a.d))
+    return FA_ERR_INVALID_ARG;
   if (a.q_weight) {
     if (!a.dq_weight || !a.dk_weight || !aligned(a.dq_weight, 4) || !aligned(a.dk_weight, 4)) return FA_ERR_INVALID_ARG;
     if (!a.workspace || a.workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(a.d) || !aligned(a.workspace, 256))

@@ -326,7 +326,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  *   dq_out [B,Hq,N,d], dk_out [B,Hkv,N,d] contiguous, of dtype dout_dtype (what fa_bwd writes).
  *   q, k by strides, of dtype `dtype` (not read without weights).
  *   dq, dk of dtype grad_dtype by dq_strides, dk_strides (the projection's layout, for example);
- *   strides of dimensions larger than 1 must be at least d, and no two rows may share memory.
+ *   no two of its rows may share memory: each dimension larger than 1 has to step past all that the
+ *   dimensions of smaller strides cover, as in any permuted slice of a dense array.
  *   dq_weight, dk_weight [d] fp32: the sums over every row of q, of k (with weights only).  The
  *   order of each sum is fixed: the same call gives the same bits.
  *   dtype BF16: dout_dtype and grad_dtype each F32 or BF16.  dtype F32: both F32.

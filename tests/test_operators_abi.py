@@ -223,3 +223,14 @@ def test_dynamic_shared_memory_is_aligned():
             aligned = re.search(r"__align__\((16|128|1024)\)", line) or "1023" in "".join(lines[i + 1 : i + 3])
             assert aligned, f"{os.path.basename(path)}:{i + 1}: {line.strip()}"
     assert seen >= 10
+
+
+@pytest.mark.parametrize("which", ["dq", "dk"])
+def test_gradient_rows_that_overlap_are_refused(L, which):
+    """dq [2, 4, 4, 64], dk [2, 2, 4, 64]: a projection's layout and permuted slices pass (to the next check)."""
+    H = 4 if which == "dq" else 2
+    for strides in ((64 * H, 64, 64 * H), (1024, 64, 64), (64, 96, 2048), (2048, 64, 64 * H - 8), (64 * 4 * H - 64, 256, 64)):
+        assert call(L, "fa_qk_norm_rope_bwd", BWD, {which + "_strides": strides, "ws": None}) == BAD, strides
+    for strides in ((64 * 4 * H, 256, 64), (4096, 64, 512), (64, 128, 128 * H), (72, 4096, 1024), (256 * H, 64, 64 * H),
+                    (2**62, 64, 512)):
+        assert call(L, "fa_qk_norm_rope_bwd", BWD, {which + "_strides": strides, "ws": None}) == WS, strides
