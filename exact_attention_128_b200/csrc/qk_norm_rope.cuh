@@ -15,11 +15,12 @@
 // token group, while the first rows are on their way; all heads' rows share them, from shared
 // memory, as they share the weights.  (With the angles of a lane's 8 pairs computed by each warp for
 // itself and kept in registers, 116 registers left 16 warps on an SM, and the prefill of 4 x 8192
-// tokens, 32 + 8 heads of 128, took 115 us instead of 111 into reused outputs, the fp32 image layer
-// 33 instead of 29.)  A warp writes 1 KB of consecutive tokens of one head.  Measured: that prefill
-// reads and writes 671 MB in 115 us, 5.8 TB/s (calls in a row into fresh outputs 123 us); the
-// backward of 8 x 4096 tokens, 16 + 16 heads of 64 with fp32 gradients in, 537 MB in 95 us, 5.6
-// TB/s, and 4 us for the weights' sums.
+// tokens, 32 + 8 heads of 128, took 4 us longer into reused outputs, the fp32 image layer 33 us instead
+// of 29.)  A warp writes 1 KB of consecutive tokens of one head.  Measured: that prefill reads and
+// writes 671 MB in 110 us into reused outputs, 6.1 TB/s (without norm 105), and in 118 to 125 us in
+// calls in a row into fresh ones; the backward of 8 x 4096 tokens, 16 + 16 heads of 64 with fp32
+// gradients in, 537 MB in 95 us with the weights' sums (without norm 65); in fp32 throughout, 805 MB in
+// 133 us, 6.0 TB/s.
 //
 // Angles: the position (up to 2^31) times the frequency is taken in turns in 64 bits and reduced
 // to [-1/2, 1/2] before it is rounded to 32 bits, so far positions lose nothing (and where the results
@@ -33,7 +34,7 @@ namespace rope {
 constexpr int THREADS = 256;
 constexpr int MAX_CHUNK = 16;  // backward: heads of a unit, at most
 // Rows a thread has in flight, + 1.  Forward: 3 CTAs on an SM; more stages or a fourth CTA at 64
-// registers were slower (prefill of 4 x 8192: 111 us; 7 stages 115, 4 CTAs 130).  Backward: 2 CTAs
+// registers were slower (prefill of 4 x 8192: 110 us; 7 stages 115, 4 CTAs 130).  Backward: 2 CTAs
 // of 128 registers; the forward's form, with angles and weights read from shared memory, took 99 us
 // on the training step (2 CTAs; 3 CTAs 142 to 149), this one 93.
 constexpr int FWD_STAGES = 5, FWD_STAGES_F32 = 4, FWD_CTAS = 3;

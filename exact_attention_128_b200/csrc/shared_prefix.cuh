@@ -17,12 +17,14 @@
 //   warps 2-9  softmax of row tiles 0 and 1, one thread per row.
 // Scores are double-buffered in TMEM and issued one key tile ahead, so a softmax warp goes from
 // one tile to the next without waiting for its own P V (with one buffer, the chain S, softmax,
-// P V of a 64-key tile took 3290 cycles a step of two row tiles; MMAs alone take about 1100).
+// P V of a 64-key tile took 3290 cycles a step of two row tiles where two took 2150, with one product).
 // Only the rare step whose maximum rises waits for the P V before it, to rescale u.
-// What bounds it: Q is read from shared memory again for every 64-key tile, and with K and V that
-// saturates shared memory: a step of two row tiles takes about 2150 cycles, of which the MMAs need
-// 1030 and the exponentials 1024.  256 requests of 32 heads, 8 kv heads, 16384 shared tokens: 83 us,
-// 830 TFLOP/s at the clocks of a short run; with the own tokens and the join 139 to 145 us power-capped.
+// What bounds it: the chain S, P V of a row tile.  Its MMAs need 1540 cycles a step of two row tiles at
+// the full rate, but S reads Q from shared memory again for every 64-key tile, 192 bytes a cycle where
+// there are 128, and each hand-over between the MMA warp and the softmax costs some 200; the exponentials,
+// 1024 cycles, run beside it.  A step takes 1.9 us (1.5 with one product).  256 requests of 32 heads, 8 kv heads,
+// 16384 shared tokens: 107 us, 640 TFLOP/s, the tensor pipe 48 % busy; with the own tokens and the join
+// 142 us in short runs, 165 to 167 power-capped.
 // BN = 64 and two K/V stages keep the CTA at 150 KB of shared memory and 352 threads of at most
 // 104 registers, so that a CTA of the requests' own (memory-bound) part runs on the SM beside it.
 // P is multiplied as the sum of two bf16 parts, its rounding and the rest, as in the pieces
@@ -90,8 +92,9 @@ struct PrefixBars {
 };
 static_assert(sizeof(PrefixBars) <= 256, "barrier area");
 
-// (104 registers, so that the register file holds a CTA of the requests' own part too: 96 and 112
-// take the same time, with 120 it does not fit beside this one: 139 -> 142 us for 256 requests)
+// (104 registers, so that the register file holds a CTA of the requests' own part too.  With one product
+// of P: 96 and 112 took the same time, with 120 it did not fit beside this one, 3 us more for 256
+// requests.  With two, a few values spill: 36 bytes at d = 128.)
 template <int D>
 __global__ void __maxnreg__(104)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
